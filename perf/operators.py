@@ -124,7 +124,7 @@ def _select(l, k):
     """Ids of the k largest (ties to the lowest index), -1 where nothing is left."""
     v, i = torch.sort(l.float(), dim=1, descending=True, stable=True)
     v, i = v[:, :k], i[:, :k]
-    ok = v > -math.inf
+    ok = v != -math.inf
     return v, torch.where(ok, i, torch.full_like(i, -1)), ok
 
 
