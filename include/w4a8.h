@@ -51,7 +51,7 @@ typedef enum {
   W4A8_OK = 0,
   W4A8_ERR_NULL = 1,      /* a required pointer is NULL */
   W4A8_ERR_SHAPE = 2,     /* E, N, K, T or top_k outside the supported range */
-  W4A8_ERR_LAYOUT = 3,    /* unknown a_scale_layout */
+  W4A8_ERR_LAYOUT = 3,    /* unknown scale layout, weight format, logits type or score */
   W4A8_ERR_ALIGN = 4,     /* a pointer is not aligned as documented */
   W4A8_ERR_CAPACITY = 5,  /* a caller buffer is too small */
   W4A8_ERR_DEVICE = 6,    /* current device is not gfx950 or cannot be queried */
@@ -64,11 +64,18 @@ enum {
   W4A8_SCALE_M_MAJOR = 1    /* a_scales fp32 [K/128][R]: SA(r,g) at g*R+r, R = offsets[E] */
 };
 
-/* Weight-scale formats of w4a8_grouped_gemm_a16. */
+/* Weight-scale formats of w4a8_grouped_gemm_a16 (the first two) and w4a8_matvec. */
 enum {
   W4A8_WSCALE_MX = 0,  /* MXFP4: E8M0 code per (expert, column, 32 K), value 2^(code-127) */
-  W4A8_WSCALE_NV = 1   /* NVFP4: E4M3FN code per (expert, column, 16 K) */
+  W4A8_WSCALE_NV = 1,  /* NVFP4: E4M3FN code per (expert, column, 16 K) */
+  W4A8_WSCALE_INT4 = 2 /* codes 0..15 with a bf16 scale per (expert, column, 32, 64 or 128 K) */
 };
+
+/* Types of the router's logits. */
+enum { W4A8_TYPE_F32 = 0, W4A8_TYPE_BF16 = 1 };
+
+/* Scores of the router's gate. */
+enum { W4A8_GATE_SOFTMAX = 0, W4A8_GATE_SIGMOID = 1 };
 
 /* Limits of this version. */
 #define W4A8_MAX_EXPERTS 2048        /* grouped GEMM: per-expert tables live in LDS */
@@ -76,6 +83,9 @@ enum {
                                         may lower it on a device (W4A8_ERR_CAPACITY) */
 #define W4A8_MAX_K 1048576     /* keeps every in-tile byte offset within 32 bits */
 #define W4A8_MAX_N 16777216    /* keeps work-item counts within 32 bits */
+#define W4A8_MAX_GATE_EXPERTS 16384  /* topk_gate: a row lives in one workgroup's registers */
+#define W4A8_MAX_GATE_TOP_K 64       /* topk_gate: a wave holds one pick per lane */
+#define W4A8_MAX_MATVEC_SLOTS 64     /* matvec: a wave holds one slot per lane */
 
 /*
  * w4a8_route_prep -- routing histogram, exclusive-scan offsets and row map.
@@ -381,6 +391,167 @@ int w4a8_grouped_gemm_swiglu(const uint8_t* A_fp8_dev, const float* a_scales_dev
 int w4a8_grouped_gemm_a16(const uint16_t* A_bf16_dev, const uint8_t* B_fp4_dev, const uint8_t* b_scales_dev,
                           int b_scale_format, const float* expert_scales_dev, const int32_t* expert_offsets_dev,
                           int E, int N, int K, uint16_t* C_bf16_dev, void* stream);
+
+/*
+ * w4a8_topk_gate -- the router's gate: the top_k experts of every token and
+ * their weights, from the router's logits.
+ *
+ * logits_dev   [T][E], fp32 (W4A8_TYPE_F32) or bf16 (W4A8_TYPE_BF16).
+ *              Aligned to its type.
+ * ids_dev      out int32 [T][top_k]: the experts by descending logit, equal
+ *              logits by ascending expert (the input of w4a8_route_prep and
+ *              w4a8_matvec).
+ * weights_dev  out fp32 [T][top_k] (the input of w4a8_combine).
+ * With l the token's logits, i the selected experts:
+ *   softmax           w_i = scale * e^l_i / sum over all e of e^l_e
+ *   softmax, renorm   w_i = scale * e^l_i / sum over the selected
+ *   sigmoid           w_i = scale * s(l_i), s(v) = 1 / (1 + e^-v)
+ *   sigmoid, renorm   w_i = scale * s(l_i) / sum over the selected
+ * in fp32 (no overflow for any finite logits).  A logit of -inf closes an
+ * expert: it is never selected; where fewer than top_k are open the rest of
+ * the row is id -1, weight 0 (all of it for a token with none).  Finite
+ * values are ordinary logits, the type's lowest among them.  NaN sorts before
+ * +inf and its weight is NaN, as are all of the row's where they share a
+ * sum; so are the weights of a softmax row with +inf.
+ * Limits: T >= 0, 1 <= E <= W4A8_MAX_GATE_EXPERTS, 1 <= top_k <= min(E,
+ * W4A8_MAX_GATE_TOP_K), T*top_k < 2^31.  T == 0 does nothing.
+ */
+int w4a8_topk_gate(const void* logits_dev, int logits_type, int T, int E, int top_k, int score, int renorm,
+                   float scale, int32_t* ids_dev, float* weights_dev, void* stream);
+
+/*
+ * w4a8_topk_gate_backward -- the logits' gradient from the weights' gradient
+ * dweights fp32 [T][top_k] (w4a8_combine_backward's); the selection is a
+ * constant.  logits, score, renorm and scale as in the forward call, ids its
+ * result.  Slots whose id is outside [0, E) take no part.
+ * dlogits_dev  out [T][E] in the logits' type, every element written: zero
+ *              outside the selection, except that softmax without renorm
+ *              reaches every expert with a finite logit.  fp32 inside, one
+ *              rounding.
+ * Limits and alignment as w4a8_topk_gate.
+ */
+int w4a8_topk_gate_backward(const void* logits_dev, int logits_type, int T, int E, const int32_t* ids_dev,
+                            const float* dweights_dev, int top_k, int score, int renorm, float scale,
+                            void* dlogits_dev, void* stream);
+
+/*
+ * w4a8_dispatch -- bf16 tokens copied to the grouped row of every (token,
+ * slot): A[row_of_slot[t*top_k + j], :] = x[t, :], the input of
+ * w4a8_grouped_gemm_a16 (w4a8_quantize_gather is its FP8 counterpart).
+ *
+ * x_bf16_dev       bf16 [T][K].
+ * row_of_slot_dev  int32 [T*top_k] (as produced by w4a8_route_prep); slots
+ *                  whose row is outside [0, R) are skipped, no two others may
+ *                  name the same row.  4-byte aligned.
+ * A_bf16_dev       out bf16 [R][K]; rows that no slot names are left as they
+ *                  were.
+ * Limits: T >= 0, 1 <= top_k, T*top_k < 2^31, 1 <= K <= W4A8_MAX_N, R >= 0.
+ * T == 0 or R == 0 does nothing.  x and A need 2-byte alignment; with K % 8
+ * == 0 and 16-byte alignment rows move 16 bytes at a time.
+ */
+int w4a8_dispatch(const uint16_t* x_bf16_dev, int T, int K, const int32_t* row_of_slot_dev, int top_k, int R,
+                  uint16_t* A_bf16_dev, void* stream);
+
+/*
+ * w4a8_dispatch_backward -- its gradient: dx[t, :] = bf16_rne(sum over j of
+ * dA[row_of_slot[t*top_k + j], :]), summed in fp32 in slot order; a token
+ * with no row gets zeros.  dA bf16 [R][K], dx out bf16 [T][K]; the rest as
+ * w4a8_dispatch (T == 0 does nothing; rows may be shared).
+ */
+int w4a8_dispatch_backward(const uint16_t* dA_bf16_dev, int R, int K, const int32_t* row_of_slot_dev, int T,
+                           int top_k, uint16_t* dx_bf16_dev, void* stream);
+
+/*
+ * w4a8_combine_backward -- the gradients of w4a8_combine:
+ *   dC[row(t, j), :] = bf16_rne(w[t, j] * dout[t, :])   (the product in fp32),
+ *   dweights[t, j]   = sum over n of C[row(t, j), n] * dout[t, n]   (fp32).
+ *
+ * C_bf16_dev       bf16 [R][N], the forward call's input.
+ * dout_bf16_dev    bf16 [T][N].
+ * row_of_slot_dev, weights_dev: as in the forward call; no two slots may
+ *                  name the same row in [0, R).
+ * dC_bf16_dev      out bf16 [R][N]; rows that no slot names are left as they
+ *                  were.
+ * dweights_dev     out fp32 [T*top_k]; 0 for slots whose row is outside
+ *                  [0, R).
+ * Every run gives the same bits.  Limits: T >= 0, 1 <= top_k, T*top_k <
+ * 2^31, 1 <= N <= W4A8_MAX_N, R >= 0.  T == 0 does nothing.  C, dout and dC
+ * need 2-byte alignment; with N % 8 == 0 and 16-byte alignment rows move 16
+ * bytes at a time.
+ */
+int w4a8_combine_backward(const uint16_t* C_bf16_dev, const uint16_t* dout_bf16_dev, int R, int N,
+                          const int32_t* row_of_slot_dev, const float* weights_dev, int T, int top_k,
+                          uint16_t* dC_bf16_dev, float* dweights_dev, void* stream);
+
+/*
+ * w4a8_matvec -- matrix-vector products of a few tokens with 4-bit weights
+ * and group scales, for decoding: no routing prep, no grouping of rows.
+ *
+ *   y[s, n] = bf16_rne( gs[e] * sum_k x[s / (S/X), k]
+ *                               * (q(e, n, k) - z(e, n, k/group)) * sc(e, n, k/group) ),  e = ids[s]
+ *
+ * x_bf16_dev         bf16 [X][K]: row s / (S/X) serves slot s (X = tokens
+ *                    where a token's slots share its row, X = S where every
+ *                    slot has its own).  16-byte aligned.
+ * B_dev              uint8 [E][N][K/2] codes, K-contiguous per column,
+ *                    element 2j in bits 3:0.  16-byte aligned.
+ * b_scales_dev, b_scale_format, group:
+ *                    W4A8_WSCALE_MX   q E2M1, uint8 [E][N][K/32] E8M0, group 32
+ *                    W4A8_WSCALE_NV   q E2M1, uint8 [E][N][K/16] E4M3FN, group 16
+ *                    W4A8_WSCALE_INT4 q = code 0..15, bf16 [E][N][K/group],
+ *                                     group 32, 64 or 128.  4-byte aligned.
+ * zeros_dev          uint8 [E][N][K/group] zero points 0..15 of INT4 weights,
+ *                    or NULL for 8 (NULL for the other formats, z = 0).
+ * expert_scales_dev  fp32 [E] gs, or NULL for all ones.
+ * expert_ids_dev     int32 [S] (w4a8_topk_gate's ids), or NULL with E == 1;
+ *                    a slot whose id is outside [0, E) gets zeros.
+ * y_bf16_dev         out bf16 [S][N].  4-byte aligned.
+ * Sums and scales are fp32, with one rounding to bf16.  NaN scale codes make
+ * their columns NaN for the expert's slots.
+ * Limits: 0 <= S <= W4A8_MAX_MATVEC_SLOTS, S % X == 0, 1 <= E <=
+ * W4A8_MAX_PREP_EXPERTS, 1 <= N <= W4A8_MAX_N, K a multiple of group and of
+ * 32, 32 <= K <= W4A8_MAX_K.  S == 0 does nothing.
+ */
+int w4a8_matvec(const uint16_t* x_bf16_dev, int X, const uint8_t* B_dev, const void* b_scales_dev,
+                int b_scale_format, int group, const uint8_t* zeros_dev, const float* expert_scales_dev,
+                const int32_t* expert_ids_dev, int S, int E, int N, int K, uint16_t* y_bf16_dev, void* stream);
+
+/*
+ * w4a8_swiglu -- SwiGLU of the gate/up output in bf16, optionally with an
+ * 8-bit copy of its input for the backward pass.
+ *
+ * C_bf16_dev       bf16 [R][2I]: gate in columns 0 .. I-1, up in I .. 2I-1.
+ * h_bf16_dev       out bf16 [R][I]: bf16_rne(silu(g) * u), evaluated as in
+ *                  w4a8_swiglu_quant.
+ * ckpt_fp8_dev     out uint8 [R][2I] E4M3FN codes of C, or NULL (with
+ *                  ckpt_scales_dev) for no copy.
+ * ckpt_scales_dev  out fp32 [R][2I/128].  4-byte aligned.
+ * Per (row, 128 columns of C): s = amax|C| / 448 (1 where amax < 2^-100),
+ * code = E4M3FN round-to-nearest-even of C * (1/s), fp32 divisions rounded
+ * to nearest: the copy's bits are unique.  NaN keeps a NaN code; a group
+ * with an infinity gets an infinite scale and reads back as NaN.
+ * Limits: R >= 0, I % 128 == 0, 128 <= I <= W4A8_MAX_K, R * I/128 < 2^36.
+ * R == 0 does nothing.  16-byte alignment except for the scales.
+ */
+int w4a8_swiglu(const uint16_t* C_bf16_dev, int R, int I, uint16_t* h_bf16_dev, uint8_t* ckpt_fp8_dev,
+                float* ckpt_scales_dev, void* stream);
+
+/*
+ * w4a8_swiglu_backward -- the gradient of SwiGLU from the 8-bit copy that
+ * w4a8_swiglu kept: with g, u the copy's values (code * s) and s = 1 / (1 +
+ * e^-g),
+ *   dC[:, :I] = bf16_rne(dh * u * s * (1 + g * (1 - s))),
+ *   dC[:, I:] = bf16_rne(dh * g * s),   h = bf16_rne(g * s * u).
+ *
+ * ckpt_fp8_dev, ckpt_scales_dev: as w4a8_swiglu wrote them.
+ * dh_bf16_dev  bf16 [R][I].
+ * dC_bf16_dev  out bf16 [R][2I].
+ * h_bf16_dev   out bf16 [R][I], the recomputed h (for the down projection's
+ *              weight gradient), or NULL.
+ * Limits and alignment as w4a8_swiglu.
+ */
+int w4a8_swiglu_backward(const uint8_t* ckpt_fp8_dev, const float* ckpt_scales_dev, const uint16_t* dh_bf16_dev,
+                         int R, int I, uint16_t* dC_bf16_dev, uint16_t* h_bf16_dev, void* stream);
 
 /*
  * w4a8_plan_params -- the plan rule's constants, written to out_host[0..n-1]

@@ -19,15 +19,30 @@ torch when the caller does not pass them.
                                      -> A2 (E4M3 codes of silu(gate) * up), SA2
     grouped_gemm_a16(A_bf16, B, SB, fmt, expert_offsets, expert_scales=None, out=None)
                                      -> C (bf16), MXFP4 (fmt 0) or NVFP4 (fmt 1) weights
+    topk_gate(logits, top_k, score, renorm, scale) -> ids, weights of the router's selection
+    topk_gate_backward(logits, ids, dweights, score, renorm, scale) -> dlogits
+    dispatch(x, row_of_slot, top_k, R) -> A (bf16 tokens in their grouped rows)
+    dispatch_backward(dA, row_of_slot, top_k) -> dx
+    combine_backward(C, dout, row_of_slot, weights, top_k) -> dC, dweights
+    matvec(x, B, SB, fmt, expert_ids=None, expert_scales=None, zeros=None)
+                                     -> y (bf16), few tokens; MXFP4, NVFP4 or INT4 (fmt 2) weights
+    swiglu(C, checkpoint=False)      -> h (bf16), or h and an E4M3 copy of C (codes, scales)
+    swiglu_backward(codes, scales, dh, dC=None, h=None) -> dC (and h) from that copy
 """
 
 from ._lib import (  # noqa: F401
+    GATE_SIGMOID,
+    GATE_SOFTMAX,
     SCALE_M_MAJOR,
     SCALE_ROW_MAJOR,
+    WSCALE_INT4,
     WSCALE_MX,
     WSCALE_NV,
     W4A8Error,
     combine,
+    combine_backward,
+    dispatch,
+    dispatch_backward,
     grouped_gemm,
     grouped_gemm_a16,
     grouped_gemm_planned,
@@ -35,11 +50,16 @@ from ._lib import (  # noqa: F401
     grouped_gemm_swiglu,
     lib_path,
     load,
+    matvec,
     plan,
     plan_bytes,
     plan_params,
     quantize_gather,
     route_prep,
     route_prep_waves,
+    swiglu,
+    swiglu_backward,
     swiglu_quant,
+    topk_gate,
+    topk_gate_backward,
 )

@@ -56,6 +56,23 @@ def _declare(lib):
     lib.w4a8_combine.restype = i32
     lib.w4a8_quantize_gather.argtypes = [vp, i32, i32, vp, i32, i32, vp, vp, i32, vp]
     lib.w4a8_quantize_gather.restype = i32
+    f32 = ctypes.c_float
+    lib.w4a8_topk_gate.argtypes = [vp, i32, i32, i32, i32, i32, i32, f32, vp, vp, vp]
+    lib.w4a8_topk_gate.restype = i32
+    lib.w4a8_topk_gate_backward.argtypes = [vp, i32, i32, i32, vp, vp, i32, i32, i32, f32, vp, vp]
+    lib.w4a8_topk_gate_backward.restype = i32
+    lib.w4a8_dispatch.argtypes = [vp, i32, i32, vp, i32, i32, vp, vp]
+    lib.w4a8_dispatch.restype = i32
+    lib.w4a8_dispatch_backward.argtypes = [vp, i32, i32, vp, i32, i32, vp, vp]
+    lib.w4a8_dispatch_backward.restype = i32
+    lib.w4a8_combine_backward.argtypes = [vp, vp, i32, i32, vp, vp, i32, i32, vp, vp, vp]
+    lib.w4a8_combine_backward.restype = i32
+    lib.w4a8_matvec.argtypes = [vp, i32, vp, vp, i32, i32, vp, vp, vp, i32, i32, i32, i32, vp, vp]
+    lib.w4a8_matvec.restype = i32
+    lib.w4a8_swiglu.argtypes = [vp, i32, i32, vp, vp, vp, vp]
+    lib.w4a8_swiglu.restype = i32
+    lib.w4a8_swiglu_backward.argtypes = [vp, vp, vp, i32, i32, vp, vp, vp]
+    lib.w4a8_swiglu_backward.restype = i32
     lib.w4a8_plan_params.argtypes = [ctypes.POINTER(ctypes.c_int32), i32]
     lib.w4a8_plan_params.restype = i32
     lib.w4a8_status_string.argtypes = [i32]
@@ -405,3 +422,226 @@ def swiglu_quant(C: torch.Tensor, layout: int, A: Optional[torch.Tensor] = None,
     _need(SA, "a_scales", torch.float32, R * (I // 128))
     _check("w4a8_swiglu_quant", lib.w4a8_swiglu_quant(_ptr(C), R, I, _ptr(A), _ptr(SA), int(layout), _stream()))
     return A, SA
+
+
+GATE_SOFTMAX = 0
+GATE_SIGMOID = 1
+
+
+def _logits_type(t: torch.Tensor) -> int:
+    if t.dim() != 2:
+        raise ValueError("logits must be [T, E]")
+    if t.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"logits must be float32 or bfloat16, got {t.dtype}")
+    return 0 if t.dtype == torch.float32 else 1
+
+
+def _bf16(t: torch.Tensor, name: str, numel: Optional[int] = None):
+    if isinstance(t, torch.Tensor) and t.dtype not in (torch.bfloat16, torch.uint16, torch.int16):
+        raise TypeError(f"{name} must be bfloat16 (or 16-bit integer bits)")
+    _need(t, name, getattr(t, "dtype", None), numel)
+
+
+def topk_gate(logits: torch.Tensor, top_k: int, score: int = GATE_SOFTMAX, renorm: bool = True, scale: float = 1.0,
+              ids: Optional[torch.Tensor] = None, weights: Optional[torch.Tensor] = None):
+    """Router logits [T, E] (fp32 or bf16) -> (ids int32 [T, top_k] by
+    descending logit, ties to the lower expert; weights fp32 [T, top_k]).
+    Weights are scale times the softmax over all experts or the sigmoid, with
+    renorm divided by their sum over the selected; -inf closes an expert, and
+    a slot with nothing left is id -1, weight 0."""
+    lib = load()
+    kind = _logits_type(logits)
+    T, E = logits.shape
+    _need(logits, "logits", logits.dtype)
+    if ids is None:
+        ids = torch.empty((T, top_k), dtype=torch.int32, device=logits.device)
+    if weights is None:
+        weights = torch.empty((T, top_k), dtype=torch.float32, device=logits.device)
+    _need(ids, "ids", torch.int32, T * top_k)
+    _need(weights, "weights", torch.float32, T * top_k)
+    _check("w4a8_topk_gate", lib.w4a8_topk_gate(_ptr(logits), kind, T, E, int(top_k), int(score), int(renorm),
+                                                float(scale), _ptr(ids), _ptr(weights), _stream()))
+    return ids, weights
+
+
+def topk_gate_backward(logits: torch.Tensor, ids: torch.Tensor, dweights: torch.Tensor, score: int = GATE_SOFTMAX,
+                       renorm: bool = True, scale: float = 1.0, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """dlogits [T, E] (the logits' type) from dweights fp32 [T, top_k]; logits,
+    score, renorm and scale as given to topk_gate, ids as it returned them."""
+    lib = load()
+    kind = _logits_type(logits)
+    T, E = logits.shape
+    _need(logits, "logits", logits.dtype)
+    if ids.dim() != 2 or ids.shape[0] != T:
+        raise ValueError("ids must be [T, top_k]")
+    k = ids.shape[1]
+    _need(ids, "ids", torch.int32)
+    _need(dweights, "dweights", torch.float32, T * k)
+    if out is None:
+        out = torch.empty_like(logits)
+    _need(out, "out", logits.dtype, T * E)
+    _check("w4a8_topk_gate_backward", lib.w4a8_topk_gate_backward(
+        _ptr(logits), kind, T, E, _ptr(ids), _ptr(dweights), k, int(score), int(renorm), float(scale), _ptr(out),
+        _stream()))
+    return out
+
+
+def _slots(row_of_slot: torch.Tensor, top_k: int) -> int:
+    if top_k < 1 or row_of_slot.numel() % top_k:
+        raise ValueError("row_of_slot must hold T * top_k entries")
+    _need(row_of_slot, "row_of_slot", torch.int32)
+    return row_of_slot.numel() // top_k
+
+
+def dispatch(x: torch.Tensor, row_of_slot: torch.Tensor, top_k: int, R: int,
+             out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """bf16 tokens x [T, K] -> A bf16 [R, K], every token copied to the rows of
+    its slots (row_of_slot int32 [T * top_k]; slots without a row are skipped,
+    rows without a slot keep what `out` holds, zeros where it is not given)."""
+    lib = load()
+    if x.dim() != 2:
+        raise ValueError("x must be [T, K]")
+    T, K = x.shape
+    _bf16(x, "x")
+    _need(row_of_slot, "row_of_slot", torch.int32, T * top_k)
+    if out is None:
+        out = torch.zeros((R, K), dtype=torch.bfloat16, device=x.device)
+    _bf16(out, "out", R * K)
+    _check("w4a8_dispatch", lib.w4a8_dispatch(_ptr(x), T, K, _ptr(row_of_slot), int(top_k), int(R), _ptr(out),
+                                              _stream()))
+    return out
+
+
+def dispatch_backward(dA: torch.Tensor, row_of_slot: torch.Tensor, top_k: int,
+                      out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """dx bf16 [T, K] of dispatch: every token's sum of its slots' rows of dA
+    bf16 [R, K], in fp32, rounded once."""
+    lib = load()
+    if dA.dim() != 2:
+        raise ValueError("dA must be [R, K]")
+    R, K = dA.shape
+    _bf16(dA, "dA")
+    T = _slots(row_of_slot, top_k)
+    if out is None:
+        out = torch.empty((T, K), dtype=torch.bfloat16, device=dA.device)
+    _bf16(out, "out", T * K)
+    _check("w4a8_dispatch_backward", lib.w4a8_dispatch_backward(_ptr(dA), R, K, _ptr(row_of_slot), T, int(top_k),
+                                                                _ptr(out), _stream()))
+    return out
+
+
+def combine_backward(C: torch.Tensor, dout: torch.Tensor, row_of_slot: torch.Tensor, weights: torch.Tensor,
+                     top_k: int, dC: Optional[torch.Tensor] = None, dweights: Optional[torch.Tensor] = None):
+    """Gradients of combine: (dC bf16 [R, N] = weight * dout in the row of each
+    slot, dweights fp32 [T * top_k] = <C row, dout row>, 0 for slots without a
+    row).  Rows of dC without a slot keep what dC holds, zeros where it is not
+    given."""
+    lib = load()
+    if C.dim() != 2 or dout.dim() != 2 or dout.shape[1] != C.shape[1]:
+        raise ValueError("C must be [R, N] and dout [T, N]")
+    R, N = C.shape
+    T = _slots(row_of_slot, top_k)
+    _bf16(C, "C")
+    _bf16(dout, "dout", T * N)
+    _need(weights, "weights", torch.float32, T * top_k)
+    if dC is None:
+        dC = torch.zeros((R, N), dtype=torch.bfloat16, device=C.device)
+    if dweights is None:
+        dweights = torch.empty(T * top_k, dtype=torch.float32, device=C.device)
+    _bf16(dC, "dC", R * N)
+    _need(dweights, "dweights", torch.float32, T * top_k)
+    _check("w4a8_combine_backward", lib.w4a8_combine_backward(
+        _ptr(C), _ptr(dout), R, N, _ptr(row_of_slot), _ptr(weights), T, int(top_k), _ptr(dC), _ptr(dweights),
+        _stream()))
+    return dC, dweights
+
+
+WSCALE_INT4 = 2  # integer codes 0..15, bf16 scale per 32, 64 or 128 K (matvec)
+
+
+def matvec(x: torch.Tensor, B: torch.Tensor, SB: torch.Tensor, fmt: int, expert_ids: Optional[torch.Tensor] = None,
+           expert_scales: Optional[torch.Tensor] = None, zeros: Optional[torch.Tensor] = None,
+           out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y[S, N] (bf16) of a few tokens with 4-bit weights: slot s multiplies row
+    s // (S / X) of x bf16 [X, K] with the weights of expert expert_ids[s]
+    (int32, S = their number, at most 64; an id outside [0, E) gives zeros;
+    None: one weight matrix, S = X).  B uint8 [E, N, K/2]; SB uint8 [E, N,
+    K/32] E8M0 (fmt WSCALE_MX), uint8 [E, N, K/16] E4M3 (WSCALE_NV) or bf16
+    [E, N, K/group] (WSCALE_INT4) with optional zeros uint8 of the same shape
+    (8 where not given); expert_scales fp32 [E] or None."""
+    lib = load()
+    if x.dim() != 2 or B.dim() != 3 or SB.dim() != 3:
+        raise ValueError("x must be [X, K], B [E, N, K/2], SB [E, N, K/group]")
+    X, K = x.shape
+    E, N, Kh = B.shape
+    if Kh * 2 != K or SB.shape[:2] != B.shape[:2]:
+        raise ValueError("inconsistent shapes of x, B and SB")
+    groups = SB.shape[2]
+    if groups < 1 or K % groups:
+        raise ValueError("SB must hold a whole number of groups of K")
+    _bf16(x, "x")
+    _need(B, "B", torch.uint8)
+    _need(SB, "b_scales", torch.bfloat16 if fmt == WSCALE_INT4 else torch.uint8)
+    if zeros is not None:
+        _need(zeros, "zeros", torch.uint8, E * N * groups)
+    if expert_scales is not None:
+        _need(expert_scales, "expert_scales", torch.float32, E)
+    S = X
+    if expert_ids is not None:
+        _need(expert_ids, "expert_ids", torch.int32)
+        S = expert_ids.numel()
+    if out is None:
+        out = torch.empty((S, N), dtype=torch.bfloat16, device=x.device)
+    _bf16(out, "out", S * N)
+    _check("w4a8_matvec", lib.w4a8_matvec(
+        _ptr(x), X, _ptr(B), _ptr(SB), int(fmt), K // groups, _ptr(zeros), _ptr(expert_scales), _ptr(expert_ids), S, E,
+        N, K, _ptr(out), _stream()))
+    return out
+
+
+def swiglu(C: torch.Tensor, checkpoint: bool = False, h: Optional[torch.Tensor] = None,
+           codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None):
+    """Gate/up output C bf16 [R, 2I] (gate columns first) -> h bf16 [R, I] =
+    silu(gate) * up; with checkpoint, (h, codes uint8 [R, 2I], scales fp32
+    [R, 2I/128]): an E4M3 copy of C for swiglu_backward."""
+    lib = load()
+    if C.dim() != 2 or C.shape[1] % 2:
+        raise ValueError("C must be [R, 2I]")
+    R, I = C.shape[0], C.shape[1] // 2
+    _bf16(C, "C")
+    if not checkpoint and (codes is not None or scales is not None):
+        raise ValueError("codes and scales go with checkpoint=True")
+    if h is None:
+        h = torch.empty((R, I), dtype=torch.bfloat16, device=C.device)
+    _bf16(h, "h", R * I)
+    if checkpoint:
+        if codes is None:
+            codes = torch.empty((R, 2 * I), dtype=torch.uint8, device=C.device)
+        if scales is None:
+            scales = torch.empty((R, 2 * I // 128), dtype=torch.float32, device=C.device)
+        _need(codes, "codes", torch.uint8, R * 2 * I)
+        _need(scales, "scales", torch.float32, R * (2 * I // 128))
+    _check("w4a8_swiglu", lib.w4a8_swiglu(_ptr(C), R, I, _ptr(h), _ptr(codes), _ptr(scales), _stream()))
+    return (h, codes, scales) if checkpoint else h
+
+
+def swiglu_backward(codes: torch.Tensor, scales: torch.Tensor, dh: torch.Tensor, dC: Optional[torch.Tensor] = None,
+                    h: Optional[torch.Tensor] = None):
+    """dC bf16 [R, 2I] of swiglu from its 8-bit copy (codes uint8 [R, 2I],
+    scales fp32 [R, 2I/128]) and dh bf16 [R, I].  With h (bf16 [R, I]) given,
+    the recomputed h is written there and (dC, h) returned."""
+    lib = load()
+    if dh.dim() != 2:
+        raise ValueError("dh must be [R, I]")
+    R, I = dh.shape
+    _bf16(dh, "dh")
+    _need(codes, "codes", torch.uint8, R * 2 * I)
+    _need(scales, "scales", torch.float32, R * (2 * I // 128))
+    if dC is None:
+        dC = torch.empty((R, 2 * I), dtype=torch.bfloat16, device=dh.device)
+    _bf16(dC, "dC", R * 2 * I)
+    if h is not None:
+        _bf16(h, "h", R * I)
+    _check("w4a8_swiglu_backward", lib.w4a8_swiglu_backward(_ptr(codes), _ptr(scales), _ptr(dh), R, I, _ptr(dC),
+                                                            _ptr(h), _stream()))
+    return dC if h is None else (dC, h)

@@ -84,6 +84,27 @@ int device_info(const DeviceInfo** out) {
   return W4A8_OK;
 }
 
+// Shapes of the slot-indexed entry points (T tokens of top_k slots each).
+int check_slots(int T, int top_k, int R, int width, const char* name) {
+  if (T < 0 || top_k < 1 || R < 0) return fail(W4A8_ERR_SHAPE, "T=%d top_k=%d R=%d", T, top_k, R);
+  if ((int64_t)T * top_k >= (int64_t)1 << 31) return fail(W4A8_ERR_SHAPE, "T*top_k too large");
+  if (width < 1 || width > W4A8_MAX_N) return fail(W4A8_ERR_SHAPE, "%s=%d outside [1, %d]", name, width, W4A8_MAX_N);
+  return W4A8_OK;
+}
+
+int check_gate(int logits_type, int T, int E, int top_k, int score) {
+  if (T < 0 || E < 1 || E > W4A8_MAX_GATE_EXPERTS)
+    return fail(W4A8_ERR_SHAPE, "T=%d, E=%d outside [1, %d]", T, E, W4A8_MAX_GATE_EXPERTS);
+  if (top_k < 1 || top_k > E || top_k > W4A8_MAX_GATE_TOP_K)
+    return fail(W4A8_ERR_SHAPE, "top_k=%d outside [1, min(E, %d)]", top_k, W4A8_MAX_GATE_TOP_K);
+  if ((int64_t)T * top_k >= (int64_t)1 << 31) return fail(W4A8_ERR_SHAPE, "T*top_k too large");
+  if (logits_type != W4A8_TYPE_F32 && logits_type != W4A8_TYPE_BF16)
+    return fail(W4A8_ERR_LAYOUT, "logits_type=%d is neither fp32 (0) nor bf16 (1)", logits_type);
+  if (score != W4A8_GATE_SOFTMAX && score != W4A8_GATE_SIGMOID)
+    return fail(W4A8_ERR_LAYOUT, "score=%d is neither softmax (0) nor sigmoid (1)", score);
+  return W4A8_OK;
+}
+
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 int check_gemm_shape(int E, int N, int K, int max_experts = W4A8_MAX_EXPERTS) {
@@ -389,6 +410,176 @@ int w4a8_swiglu_quant(const uint16_t* C_bf16_dev, int R, int I, uint8_t* A_fp8_d
   hipError_t e = w4a8::launch_swiglu_quant(C_bf16_dev, R, I, A_fp8_dev, a_scales_dev, a_scale_layout,
                                            (hipStream_t)stream);
   if (e != hipSuccess) return fail(W4A8_ERR_HIP, "swiglu_quant launch: %s", hipGetErrorString(e));
+  return ok();
+}
+
+int w4a8_topk_gate(const void* logits_dev, int logits_type, int T, int E, int top_k, int score, int renorm,
+                   float scale, int32_t* ids_dev, float* weights_dev, void* stream) {
+  int st = check_gate(logits_type, T, E, top_k, score);
+  if (st != W4A8_OK) return st;
+  if (T > 0 && (!logits_dev || !ids_dev || !weights_dev)) return fail(W4A8_ERR_NULL, "null pointer argument");
+  if (!aligned(logits_dev, logits_type == W4A8_TYPE_BF16 ? 2 : 4) || !aligned(ids_dev, 4) || !aligned(weights_dev, 4))
+    return fail(W4A8_ERR_ALIGN, "logits need the alignment of their type, ids and weights 4 bytes");
+  const DeviceInfo* d = nullptr;
+  st = device_info(&d);
+  if (st != W4A8_OK) return st;
+  if (T == 0) return ok();
+  hipError_t e = w4a8::launch_topk_gate(logits_dev, logits_type == W4A8_TYPE_BF16, T, E, top_k, score, renorm != 0,
+                                        scale, ids_dev, weights_dev, (hipStream_t)stream);
+  if (e != hipSuccess) return fail(W4A8_ERR_HIP, "topk_gate launch: %s", hipGetErrorString(e));
+  return ok();
+}
+
+int w4a8_topk_gate_backward(const void* logits_dev, int logits_type, int T, int E, const int32_t* ids_dev,
+                            const float* dweights_dev, int top_k, int score, int renorm, float scale,
+                            void* dlogits_dev, void* stream) {
+  int st = check_gate(logits_type, T, E, top_k, score);
+  if (st != W4A8_OK) return st;
+  if (T > 0 && (!logits_dev || !ids_dev || !dweights_dev || !dlogits_dev))
+    return fail(W4A8_ERR_NULL, "null pointer argument");
+  const size_t a = logits_type == W4A8_TYPE_BF16 ? 2 : 4;
+  if (!aligned(logits_dev, a) || !aligned(dlogits_dev, a) || !aligned(ids_dev, 4) || !aligned(dweights_dev, 4))
+    return fail(W4A8_ERR_ALIGN, "logits and dlogits need the alignment of their type, ids and dweights 4 bytes");
+  const DeviceInfo* d = nullptr;
+  st = device_info(&d);
+  if (st != W4A8_OK) return st;
+  if (T == 0) return ok();
+  hipError_t e = w4a8::launch_topk_gate_backward(logits_dev, logits_type == W4A8_TYPE_BF16, T, E, ids_dev,
+                                                 dweights_dev, top_k, score, renorm != 0, scale, dlogits_dev,
+                                                 (hipStream_t)stream);
+  if (e != hipSuccess) return fail(W4A8_ERR_HIP, "topk_gate_backward launch: %s", hipGetErrorString(e));
+  return ok();
+}
+
+int w4a8_dispatch(const uint16_t* x_bf16_dev, int T, int K, const int32_t* row_of_slot_dev, int top_k, int R,
+                  uint16_t* A_bf16_dev, void* stream) {
+  int st = check_slots(T, top_k, R, K, "K");
+  if (st != W4A8_OK) return st;
+  if (T > 0 && (!x_bf16_dev || !row_of_slot_dev || (R > 0 && !A_bf16_dev)))
+    return fail(W4A8_ERR_NULL, "null pointer argument");
+  if (!aligned(x_bf16_dev, 2) || !aligned(A_bf16_dev, 2) || !aligned(row_of_slot_dev, 4))
+    return fail(W4A8_ERR_ALIGN, "x and A need 2-byte, row_of_slot 4-byte alignment");
+  const DeviceInfo* d = nullptr;
+  st = device_info(&d);
+  if (st != W4A8_OK) return st;
+  if (T == 0 || R == 0) return ok();
+  hipError_t e = w4a8::launch_dispatch(x_bf16_dev, T, K, row_of_slot_dev, top_k, R, A_bf16_dev, (hipStream_t)stream);
+  if (e != hipSuccess) return fail(W4A8_ERR_HIP, "dispatch launch: %s", hipGetErrorString(e));
+  return ok();
+}
+
+int w4a8_dispatch_backward(const uint16_t* dA_bf16_dev, int R, int K, const int32_t* row_of_slot_dev, int T,
+                           int top_k, uint16_t* dx_bf16_dev, void* stream) {
+  int st = check_slots(T, top_k, R, K, "K");
+  if (st != W4A8_OK) return st;
+  if (T > 0 && (!row_of_slot_dev || !dx_bf16_dev || (R > 0 && !dA_bf16_dev)))
+    return fail(W4A8_ERR_NULL, "null pointer argument");
+  if (!aligned(dA_bf16_dev, 2) || !aligned(dx_bf16_dev, 2) || !aligned(row_of_slot_dev, 4))
+    return fail(W4A8_ERR_ALIGN, "dA and dx need 2-byte, row_of_slot 4-byte alignment");
+  const DeviceInfo* d = nullptr;
+  st = device_info(&d);
+  if (st != W4A8_OK) return st;
+  if (T == 0) return ok();
+  hipError_t e = w4a8::launch_dispatch_backward(dA_bf16_dev, R, K, row_of_slot_dev, T, top_k, dx_bf16_dev,
+                                                (hipStream_t)stream);
+  if (e != hipSuccess) return fail(W4A8_ERR_HIP, "dispatch_backward launch: %s", hipGetErrorString(e));
+  return ok();
+}
+
+int w4a8_combine_backward(const uint16_t* C_bf16_dev, const uint16_t* dout_bf16_dev, int R, int N,
+                          const int32_t* row_of_slot_dev, const float* weights_dev, int T, int top_k,
+                          uint16_t* dC_bf16_dev, float* dweights_dev, void* stream) {
+  int st = check_slots(T, top_k, R, N, "N");
+  if (st != W4A8_OK) return st;
+  if (T > 0 && (!dout_bf16_dev || !row_of_slot_dev || !weights_dev || !dweights_dev ||
+                (R > 0 && (!C_bf16_dev || !dC_bf16_dev))))
+    return fail(W4A8_ERR_NULL, "null pointer argument");
+  if (!aligned(C_bf16_dev, 2) || !aligned(dout_bf16_dev, 2) || !aligned(dC_bf16_dev, 2) ||
+      !aligned(row_of_slot_dev, 4) || !aligned(weights_dev, 4) || !aligned(dweights_dev, 4))
+    return fail(W4A8_ERR_ALIGN, "C, dout and dC need 2-byte, row_of_slot, weights and dweights 4-byte alignment");
+  const DeviceInfo* d = nullptr;
+  st = device_info(&d);
+  if (st != W4A8_OK) return st;
+  if (T == 0) return ok();
+  hipError_t e = w4a8::launch_combine_backward(C_bf16_dev, dout_bf16_dev, R, N, row_of_slot_dev, weights_dev, T,
+                                               top_k, dC_bf16_dev, dweights_dev, (hipStream_t)stream);
+  if (e != hipSuccess) return fail(W4A8_ERR_HIP, "combine_backward launch: %s", hipGetErrorString(e));
+  return ok();
+}
+
+int w4a8_matvec(const uint16_t* x_bf16_dev, int X, const uint8_t* B_dev, const void* b_scales_dev,
+                int b_scale_format, int group, const uint8_t* zeros_dev, const float* expert_scales_dev,
+                const int32_t* expert_ids_dev, int S, int E, int N, int K, uint16_t* y_bf16_dev, void* stream) {
+  if (b_scale_format != W4A8_WSCALE_MX && b_scale_format != W4A8_WSCALE_NV && b_scale_format != W4A8_WSCALE_INT4)
+    return fail(W4A8_ERR_LAYOUT, "b_scale_format=%d is none of MXFP4 (0), NVFP4 (1), INT4 (2)", b_scale_format);
+  const int fixed = b_scale_format == W4A8_WSCALE_MX ? 32 : b_scale_format == W4A8_WSCALE_NV ? 16 : 0;
+  if (fixed ? group != fixed : group != 32 && group != 64 && group != 128)
+    return fail(W4A8_ERR_SHAPE, "group=%d: MXFP4 has 32, NVFP4 16, INT4 32, 64 or 128", group);
+  if (zeros_dev && b_scale_format != W4A8_WSCALE_INT4)
+    return fail(W4A8_ERR_LAYOUT, "zero points go with INT4 weights only");
+  if (S < 0 || S > W4A8_MAX_MATVEC_SLOTS)
+    return fail(W4A8_ERR_SHAPE, "S=%d slots outside [0, %d]", S, W4A8_MAX_MATVEC_SLOTS);
+  if (S > 0 && (X < 1 || S % X)) return fail(W4A8_ERR_SHAPE, "S=%d slots are no multiple of X=%d rows", S, X);
+  if (E < 1 || E > W4A8_MAX_PREP_EXPERTS || (S > 0 && !expert_ids_dev && E != 1))
+    return fail(W4A8_ERR_SHAPE, "E=%d outside [1, %d], or above 1 without expert ids", E, W4A8_MAX_PREP_EXPERTS);
+  if (K < 32 || K % (group < 32 ? 32 : group) || K > W4A8_MAX_K)
+    return fail(W4A8_ERR_SHAPE, "K=%d must be a multiple of %d in [32, %d]", K, group < 32 ? 32 : group, W4A8_MAX_K);
+  if (N < 1 || N > W4A8_MAX_N) return fail(W4A8_ERR_SHAPE, "N=%d outside [1, %d]", N, W4A8_MAX_N);
+  if (S > 0 && (!x_bf16_dev || !B_dev || !b_scales_dev || !y_bf16_dev))
+    return fail(W4A8_ERR_NULL, "null pointer argument");
+  if (!aligned(x_bf16_dev, 16) || !aligned(B_dev, 16) || !aligned(b_scales_dev, 4) || !aligned(zeros_dev, 4) ||
+      !aligned(y_bf16_dev, 4) || !aligned(expert_scales_dev, 4) || !aligned(expert_ids_dev, 4))
+    return fail(W4A8_ERR_ALIGN, "x and B need 16-byte, the others 4-byte alignment");
+  const DeviceInfo* d = nullptr;
+  int st = device_info(&d);
+  if (st != W4A8_OK) return st;
+  if (S == 0) return ok();
+  const w4a8::MatvecArgs args{x_bf16_dev, B_dev, b_scales_dev, zeros_dev, expert_scales_dev, expert_ids_dev,
+                              y_bf16_dev, X, S, E, N, K, b_scale_format, group};
+  hipError_t e = w4a8::launch_matvec(args, (hipStream_t)stream);
+  if (e != hipSuccess) return fail(W4A8_ERR_HIP, "matvec launch: %s", hipGetErrorString(e));
+  return ok();
+}
+
+int w4a8_swiglu(const uint16_t* C_bf16_dev, int R, int I, uint16_t* h_bf16_dev, uint8_t* ckpt_fp8_dev,
+                float* ckpt_scales_dev, void* stream) {
+  if (R < 0) return fail(W4A8_ERR_SHAPE, "R=%d", R);
+  if (I < 128 || I % 128 || I > W4A8_MAX_K)
+    return fail(W4A8_ERR_SHAPE, "I=%d must be a multiple of 128 in [128, %d]", I, W4A8_MAX_K);
+  if ((int64_t)R * (I / 128) >= (int64_t)1 << 36) return fail(W4A8_ERR_SHAPE, "R * I/128 too large");
+  if (R > 0 && (!C_bf16_dev || !h_bf16_dev)) return fail(W4A8_ERR_NULL, "null pointer argument");
+  if (!ckpt_fp8_dev != !ckpt_scales_dev) return fail(W4A8_ERR_NULL, "the checkpoint's codes and scales go together");
+  if (!aligned(C_bf16_dev, 16) || !aligned(h_bf16_dev, 16) || !aligned(ckpt_fp8_dev, 16) ||
+      !aligned(ckpt_scales_dev, 4))
+    return fail(W4A8_ERR_ALIGN, "C, h and codes need 16-byte, scales 4-byte alignment");
+  const DeviceInfo* d = nullptr;
+  int st = device_info(&d);
+  if (st != W4A8_OK) return st;
+  if (R == 0) return ok();
+  hipError_t e = w4a8::launch_swiglu(C_bf16_dev, R, I, h_bf16_dev, ckpt_fp8_dev, ckpt_scales_dev,
+                                     (hipStream_t)stream);
+  if (e != hipSuccess) return fail(W4A8_ERR_HIP, "swiglu launch: %s", hipGetErrorString(e));
+  return ok();
+}
+
+int w4a8_swiglu_backward(const uint8_t* ckpt_fp8_dev, const float* ckpt_scales_dev, const uint16_t* dh_bf16_dev,
+                         int R, int I, uint16_t* dC_bf16_dev, uint16_t* h_bf16_dev, void* stream) {
+  if (R < 0) return fail(W4A8_ERR_SHAPE, "R=%d", R);
+  if (I < 128 || I % 128 || I > W4A8_MAX_K)
+    return fail(W4A8_ERR_SHAPE, "I=%d must be a multiple of 128 in [128, %d]", I, W4A8_MAX_K);
+  if ((int64_t)R * (I / 128) >= (int64_t)1 << 36) return fail(W4A8_ERR_SHAPE, "R * I/128 too large");
+  if (R > 0 && (!ckpt_fp8_dev || !ckpt_scales_dev || !dh_bf16_dev || !dC_bf16_dev))
+    return fail(W4A8_ERR_NULL, "null pointer argument");
+  if (!aligned(ckpt_fp8_dev, 16) || !aligned(dh_bf16_dev, 16) || !aligned(dC_bf16_dev, 16) ||
+      !aligned(h_bf16_dev, 16) || !aligned(ckpt_scales_dev, 4))
+    return fail(W4A8_ERR_ALIGN, "codes, dh, dC and h need 16-byte, scales 4-byte alignment");
+  const DeviceInfo* d = nullptr;
+  int st = device_info(&d);
+  if (st != W4A8_OK) return st;
+  if (R == 0) return ok();
+  hipError_t e = w4a8::launch_swiglu_backward(ckpt_fp8_dev, ckpt_scales_dev, dh_bf16_dev, R, I, dC_bf16_dev,
+                                              h_bf16_dev, (hipStream_t)stream);
+  if (e != hipSuccess) return fail(W4A8_ERR_HIP, "swiglu_backward launch: %s", hipGetErrorString(e));
   return ok();
 }
 

@@ -28,12 +28,19 @@ namespace w4a8 {
 constexpr float kLog2e = 1.44269502162933349609375f;   // fp32(log2 e)
 constexpr float kLn2Hi = 0.693147182464599609375f;     // fp32(ln 2)
 constexpr float kLn2Lo = -1.9046542121259336e-09f;     // fp32(ln 2 - kLn2Hi)
-__device__ __forceinline__ float swiglu_f32(float g, float u) {
-  const float x = fminf(fmaxf(-g, -104.0f), 104.0f);
+__device__ __forceinline__ float exp_reduced(float x) {  // |x| <= 104
   const float n = rintf(x * kLog2e);
   const float r = fmaf(-n, kLn2Lo, fmaf(-n, kLn2Hi, x));
-  const float e = ldexpf(__builtin_amdgcn_exp2f(r * kLog2e), (int)n);
+  return ldexpf(__builtin_amdgcn_exp2f(r * kLog2e), (int)n);
+}
+__device__ __forceinline__ float swiglu_f32(float g, float u) {
+  const float e = exp_reduced(fminf(fmaxf(-g, -104.0f), 104.0f));
   return g * __builtin_amdgcn_rcpf(1.0f + e) * u;
+}
+
+// e^x for any x: 0 below -104, inf above 104, NaN kept.
+__device__ __forceinline__ float exp_f32(float x) {
+  return exp_reduced(x < -104.0f ? -104.0f : x > 104.0f ? 104.0f : x);
 }
 
 // Scale of a group from its amax: amax / 448 (IEEE division), 1 if zero.

@@ -50,4 +50,33 @@ hipError_t launch_grouped_gemm_a16(const uint16_t* A, const uint8_t* B, const ui
 hipError_t launch_quant_gather(const uint16_t* x, int T, int K, const int32_t* row_of_slot, int top_k, int R,
                                uint8_t* A, float* SA, int layout, hipStream_t stream);
 
+hipError_t launch_topk_gate(const void* logits, bool bf16, int T, int E, int k, int score, int renorm, float scale,
+                            int32_t* ids, float* weights, hipStream_t stream);
+hipError_t launch_topk_gate_backward(const void* logits, bool bf16, int T, int E, const int32_t* ids,
+                                     const float* dweights, int k, int score, int renorm, float scale, void* dlogits,
+                                     hipStream_t stream);
+hipError_t launch_dispatch(const uint16_t* x, int T, int K, const int32_t* row_of_slot, int top_k, int R, uint16_t* A,
+                           hipStream_t stream);
+hipError_t launch_dispatch_backward(const uint16_t* dA, int R, int K, const int32_t* row_of_slot, int T, int top_k,
+                                    uint16_t* dx, hipStream_t stream);
+hipError_t launch_combine_backward(const uint16_t* C, const uint16_t* dout, int R, int N, const int32_t* row_of_slot,
+                                   const float* weights, int T, int top_k, uint16_t* dC, float* dweights,
+                                   hipStream_t stream);
+
+struct MatvecArgs {
+  const uint16_t* x;       // [X][K] bf16
+  const uint8_t* B;        // [E][N][K/2] 4-bit codes
+  const void* SB;          // [E][N][K/group]
+  const uint8_t* zeros;    // [E][N][K/group] or null
+  const float* gs;         // [E] or null
+  const int32_t* ids;      // [S] or null (E = 1)
+  uint16_t* y;             // [S][N] bf16
+  int X, S, E, N, K, fmt, group;
+};
+hipError_t launch_matvec(const MatvecArgs& args, hipStream_t stream);
+hipError_t launch_swiglu(const uint16_t* C, int R, int I, uint16_t* h, uint8_t* codes, float* scales,
+                         hipStream_t stream);
+hipError_t launch_swiglu_backward(const uint8_t* codes, const float* scales, const uint16_t* dh, int R, int I,
+                                  uint16_t* dC, uint16_t* h, hipStream_t stream);
+
 }  // namespace w4a8

@@ -29,6 +29,11 @@ Modules:
   a16     -- the grouped GEMM with bf16 activations and FP4 weights, MXFP4
              (E8M0 per 32) or NVFP4 (E4M3 per 16 and one fp32 scale per
              expert) scales.
+  gate    -- the router's top-k selection, weights and gradient in fp64.
+  moves   -- tokens copied to their grouped rows, and the gradients of that
+             and of the combine.
+  matvec  -- products of a few tokens with 4-bit weights and group scales.
+  swiglu8 -- SwiGLU's 8-bit input copy, and the gradient from it.
 
 Parity status: no page prints a worked example or output value for any of
 these, so every function is pinned by closed forms, invariants, exact
@@ -51,3 +56,7 @@ from .quant import bf16_bits_to_f32, e4m3_encode_rne, quantize_gather, quantize_
 from .combine import combine_ref  # noqa: F401
 from .swiglu import check_h_quant, check_swiglu_quant, h_quant_f64, silu_f64, swiglu_f64, swiglu_quant_f64  # noqa: F401
 from .a16 import FMT_MX, FMT_NV, grouped_gemm_a16_bf16, grouped_gemm_a16_f64  # noqa: F401
+from .gate import topk_gate_backward_f64, topk_gate_f64  # noqa: F401
+from .moves import combine_backward_ref, dispatch_backward_ref, dispatch_ref  # noqa: F401
+from .matvec import FMT_INT4, matvec_f64  # noqa: F401
+from .swiglu8 import checkpoint_ref, decode_f64, swiglu_backward_f64  # noqa: F401
