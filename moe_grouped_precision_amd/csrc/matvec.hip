@@ -7,15 +7,23 @@
 // INT4: q a code 0 .. 15, z its zero point (8 when none are given), s bf16
 // per 32, 64 or 128 K.  No zero point for the first two.
 //
-// One wave per (slot, column).
+// Bound by the weights' bytes: every expert that some slot names is read
+// once, whatever the number of its slots.  matvec_kernel (below) is the path;
+// matvec_plain_kernel serves rows shorter than one of its steps and rows that
+// do not fit in LDS.
 #include "w4a8_launch.h"
 
 #include <hip/hip_runtime.h>
+
+#include <algorithm>
 
 namespace w4a8 {
 namespace {
 
 typedef float v2f __attribute__((ext_vector_type(2)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
 __device__ __forceinline__ float e2m1(uint32_t c) {
   const float mag[8] = {0.f, 0.5f, 1.f, 1.5f, 2.f, 3.f, 4.f, 6.f};
@@ -23,66 +31,453 @@ __device__ __forceinline__ float e2m1(uint32_t c) {
   return (c & 8) ? -v : v;
 }
 
+// E8M0 code -> 2^(c - 127) (code 0: the subnormal 2^-127; 0xFF: NaN).
+__device__ __forceinline__ float e8m0(uint32_t c) {
+  uint32_t b = c << 23;
+  b = c == 0 ? 0x00400000u : b;
+  b = c == 0xff ? 0x7fc00000u : b;
+  return __uint_as_float(b);
+}
+
+enum { F_MX = 0, F_NV = 1, F_INT = 2 };
+
 template <int FMT>
 __device__ __forceinline__ float group_scale(const void* p, size_t i) {
-  if (FMT == 0) {
-    const uint32_t c = ((const uint8_t*)p)[i];
-    return c == 0xff ? __builtin_nanf("") : c == 0 ? __uint_as_float(0x00400000u) : __uint_as_float(c << 23);
-  }
-  if (FMT == 1) return __builtin_amdgcn_cvt_pk_f32_fp8((int)((const uint8_t*)p)[i], false)[0];
+  if (FMT == F_MX) return e8m0(((const uint8_t*)p)[i]);
+  if (FMT == F_NV) return __builtin_amdgcn_cvt_pk_f32_fp8((int)((const uint8_t*)p)[i], false)[0];
   return __uint_as_float((uint32_t)((const uint16_t*)p)[i] << 16);
 }
 
+// One wave per (slot, column).
 template <int FMT>
 __global__ void __launch_bounds__(256)
-matvec_kernel(const uint16_t* __restrict__ x, int per_row, const uint8_t* __restrict__ B, const void* __restrict__ SB,
-              int group, const uint8_t* __restrict__ zeros, const float* __restrict__ gs,
-              const int32_t* __restrict__ ids, int E, int N, int K, uint16_t* __restrict__ y) {
+matvec_plain_kernel(const MatvecArgs a) {
   const int lane = threadIdx.x & 63;
   const int n = blockIdx.x * 4 + (threadIdx.x >> 6);
   const int s = blockIdx.y;
-  if (n >= N) return;
-  const int e = ids ? ids[s] : 0;
+  if (n >= a.N) return;
+  const int e = a.ids ? a.ids[s] : 0;
   float acc = 0.f;
-  if (e >= 0 && e < E) {
-    const size_t col = (size_t)e * N + n;
-    const uint16_t* xr = x + (size_t)(s / per_row) * K;
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(B + col * (size_t)(K >> 1));
-    for (int c = lane; c < K / 8; c += 64) {  // 8 weights: inside one group
-      const size_t gi = col * (size_t)(K / group) + (8 * c) / group;
-      const float sc = group_scale<FMT>(SB, gi);
-      const float z = FMT != 2 ? 0.f : zeros ? (float)zeros[gi] : 8.f;
+  if (e >= 0 && e < a.E) {
+    const size_t col = (size_t)e * a.N + n;
+    const uint16_t* xr = a.x + (size_t)(s / (a.S / a.X)) * a.K;
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(a.B + col * (size_t)(a.K >> 1));
+    for (int c = lane; c < a.K / 8; c += 64) {  // 8 weights: inside one group
+      const size_t gi = col * (size_t)(a.K / a.group) + (8 * c) / a.group;
+      const float sc = group_scale<FMT>(a.SB, gi);
+      const float z = FMT != F_INT ? 0.f : a.zeros ? (float)a.zeros[gi] : 8.f;
       const uint32_t v = w[c];
       float part = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const uint32_t q = (v >> (4 * i)) & 15u;
-        part = fmaf(__uint_as_float((uint32_t)xr[8 * c + i] << 16), FMT == 2 ? (float)q - z : e2m1(q), part);
+        part = fmaf(__uint_as_float((uint32_t)xr[8 * c + i] << 16), FMT == F_INT ? (float)q - z : e2m1(q), part);
       }
       acc = fmaf(part, sc, acc);
     }
 #pragma unroll
     for (int i = 1; i < 64; i <<= 1) acc += __shfl_xor(acc, i, 64);
-    if (gs) acc *= gs[e];
+    if (a.gs) acc *= a.gs[e];
   }
-  if (lane == 0) y[(size_t)s * N + n] = __builtin_bit_cast(uint16_t, (__bf16)acc);
+  if (lane == 0) a.y[(size_t)s * a.N + n] = __builtin_bit_cast(uint16_t, (__bf16)acc);
+}
+
+// ---------------------------------------------------------------------------
+// The path.  A workgroup of four waves takes a run of units (expert, 16
+// columns); its waves share a unit's K in steps of 256 (wave w takes steps w,
+// w + 4, ...) and join their sums in LDS.
+//
+// Weights: per step a wave reads 16 columns x 128 bytes as two loads of eight
+// whole 128-byte lines (lane l: column l / 8, 16-byte piece l % 8, one piece
+// = 32 K), DEPTH - 1 steps ahead in registers, and turns them into the matrix
+// instruction's operand order through a private 2 KB of LDS: piece p of
+// column c at position p ^ (c / 2 % 8), so that neither side has bank
+// conflicts.  Lane 16 q + n then holds pieces 2q and 2q + 1 of column n, and
+// v_mfma_f32_16x16x32_bf16 number j of a piece takes its weights 8j .. 8j + 7.
+//
+// Weights enter the product exactly: MXFP4 as bf16 with its scale (gfx950's
+// scaled conversion), NVFP4 as bf16 E2M1 values, INT4 as 16 + q (q in the
+// mantissa of 16.0).  For the last two the scales differ within the 128 K
+// that one instruction sums over (lane groups q hold different pieces), so x
+// is laid out block-diagonally: operand row 4t + p holds token t in lane
+// group q = p and zeros in the others; the result then has one sum per
+// (token, lane group), and the scales (and the zero points, as (16 + z) times
+// the sum of x over the piece) are applied to it in fp32.  Four tokens per
+// instruction; MXFP4 takes sixteen.
+//
+// x (the rows of the unit's expert) is in LDS as bf16, zeros past K.  Where K
+// is no multiple of 256 the last step starts at K - 256: what it repeats
+// meets zeros in x.
+// ---------------------------------------------------------------------------
+constexpr int MV_THREADS = 256;
+constexpr int MV_WAVES = 4;
+constexpr int MV_STEP = 256;              // K per step of a wave
+constexpr int MV_WBUF = 2048;             // a wave's LDS for one step of weights
+constexpr int MV_DEPTH = 3;               // steps of weights in registers
+constexpr int MV_X_PAD = 16;              // rows of x start 16 bytes apart modulo 256
+
+// bytes of LDS: weights, partial sums (two units), zeros, slots, x, sums of x
+__host__ __device__ inline int mv_row_bytes(int steps) { return steps * (MV_STEP * 2) + MV_X_PAD; }
+__host__ __device__ inline int mv_lds_bytes(int steps, int rows) {
+  return MV_WAVES * MV_WBUF + 2 * MV_WAVES * rows * 16 * 4 + 64 + 64 * 4 + rows * (mv_row_bytes(steps) + steps * 32);
+}
+
+// Scale data of one step: MXFP4 the codes of the lane's two pieces, NVFP4 the
+// column's sixteen codes, INT4 its 256 / GROUP bf16 scales and zero points
+// (packed in dwords, as loaded).
+template <int FMT, int GROUP>
+struct Scales {
+  static constexpr int NG = MV_STEP / GROUP;
+  static constexpr int BYTES = FMT == F_MX ? 2 : FMT == F_NV ? 16 : 2 * NG;
+  uint32_t c[(BYTES + 3) / 4];
+  uint32_t z[FMT == F_INT ? (NG + 3) / 4 : 1];
+};
+
+__device__ __forceinline__ int wkey(int c) { return (c >> 1) & 7; }
+
+// 8 INT4 codes -> 16 + q as bf16, in the order 0 4 1 5 2 6 3 7
+__device__ __forceinline__ v4u int4_to_bf16(uint32_t w) {
+  v4u o;
+  o[0] = ((w << 3) & 0x00780078u) | 0x41804180u;
+  o[1] = ((w >> 1) & 0x00780078u) | 0x41804180u;
+  o[2] = ((w >> 5) & 0x00780078u) | 0x41804180u;
+  o[3] = ((w >> 9) & 0x00780078u) | 0x41804180u;
+  return o;
+}
+__device__ __forceinline__ v4u fp4_to_bf16(uint32_t w, float s) {
+  v4u o;
+  o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0));
+  o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1));
+  o[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2));
+  o[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3));
+  return o;
+}
+__device__ __forceinline__ v4f mfma(v4u x, v4u w, v4f c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, x), __builtin_bit_cast(v8bf, w), c, 0, 0, 0);
+}
+
+// LDS only: every wave's LDS work done, global loads left in flight
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// position of the i-th set bit of m (i below its number of set bits)
+__device__ __forceinline__ int nth_bit(uint64_t m, int i) {
+  for (; i > 0; --i) m &= m - 1;
+  return __ffsll((unsigned long long)m) - 1;
+}
+
+// TB: sets of four tokens (MXFP4: one set of sixteen, TB = 1).
+template <int FMT, int GROUP, int TB>
+__global__ void __launch_bounds__(MV_THREADS, 4)
+matvec_kernel(const MatvecArgs a, int rows_max) {
+  constexpr bool DIAG = FMT != F_MX;
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int n16 = lane & 15, q = lane >> 4;
+  const int NP = a.K >> 5;                            // pieces of 32 K
+  const int steps = (a.K + MV_STEP - 1) / MV_STEP;
+  const int mine = (steps - wave + MV_WAVES - 1) / MV_WAVES;   // this wave's steps of a unit
+  const int pitch = mv_row_bytes(steps);
+  uint8_t* wbuf = lds + wave * MV_WBUF;
+  float* red = reinterpret_cast<float*>(lds + MV_WAVES * MV_WBUF);
+  uint8_t* zero = reinterpret_cast<uint8_t*>(red + 2 * MV_WAVES * rows_max * 16);
+  int* slots = reinterpret_cast<int*>(zero + 64);
+  uint8_t* xs = reinterpret_cast<uint8_t*>(slots + 64);
+  float* xsum = reinterpret_cast<float*>(xs + rows_max * pitch);   // [row][steps * 8]
+  if (tid < 16) reinterpret_cast<uint32_t*>(zero)[tid] = 0u;
+
+  // the experts that some slot names, in the order of their first slots
+  int id = lane < a.S ? (a.ids ? a.ids[lane] : 0) : -1;
+  if (id >= a.E) id = -1;
+  bool first = id >= 0;
+  for (int i = 0; i < a.S; ++i)
+    if (__builtin_amdgcn_readlane(id, i) == id && i < lane) first = false;
+  const uint64_t leaders = __ballot(first);
+  const int D = __popcll(leaders);
+  const int UB = (a.N + 15) >> 4;                     // units of an expert
+  const int64_t U = (int64_t)D * UB;
+  const int64_t u0 = U * blockIdx.x / gridDim.x, u1 = U * (blockIdx.x + 1) / gridDim.x;
+
+  // slots without an expert: zeros
+  for (uint64_t m = __ballot(lane < a.S && id < 0); m; m &= m - 1) {
+    const int s = __ffsll((unsigned long long)m) - 1;
+    for (int64_t n = (int64_t)blockIdx.x * MV_THREADS + tid; n < a.N; n += (int64_t)gridDim.x * MV_THREADS)
+      a.y[(size_t)s * a.N + n] = 0;
+  }
+
+  const int per_row = a.S / a.X;
+  int parity = 0;
+  for (int64_t u = u0; u < u1;) {
+    const int d = (int)(u / UB);
+    const int cb0 = (int)(u - (int64_t)d * UB);
+    const int nu = (int)min((int64_t)(UB - cb0), u1 - u);   // units of this expert here
+    const int leader = nth_bit(leaders, d);
+    const int e = __builtin_amdgcn_readlane(id, leader);
+    const uint64_t members = __ballot(id == e);
+    const int M = __popcll(members);
+    const float gs = a.gs ? a.gs[e] : 1.0f;
+    const uint8_t* Be = a.B + (size_t)e * a.N * (size_t)(a.K >> 1);
+    const size_t sstride = (size_t)(a.K / GROUP) * (FMT == F_INT ? 2 : 1);   // scale bytes of a column
+    const uint8_t* Se = (const uint8_t*)a.SB + (size_t)e * a.N * sstride;
+    const uint8_t* Ze = FMT == F_INT && a.zeros ? a.zeros + (size_t)e * a.N * (size_t)(a.K / GROUP) : nullptr;
+
+    for (int r0 = 0; r0 < M; r0 += rows_max) {
+      const int rows = min(rows_max, M - r0);
+      lds_barrier();   // the previous pass's x and slots are no longer read
+      if (wave == 0) {
+        const int rank = __popcll(members & ((1ull << lane) - 1)) - r0;
+        if (((members >> lane) & 1) && rank >= 0 && rank < rows) slots[rank] = lane;
+      }
+      // x: rows of steps * 8 pieces of 64 bytes, four lanes per piece
+      const int units16 = steps * 32;
+      for (int r = 0; r < rows; ++r) {
+        const int s = nth_bit(members, r0 + r);
+        const uint16_t* xr = a.x + (size_t)(s / per_row) * a.K;
+        for (int v = tid; v < units16; v += MV_THREADS) {
+          const int sp = v >> 2, st = sp >> 3;
+          const int p = min(8 * st, NP - 8) + (sp & 7);
+          v4u w = {0u, 0u, 0u, 0u};
+          if (p >= 8 * st) w = *reinterpret_cast<const v4u*>(xr + (size_t)p * 32 + (v & 3) * 8);
+          if (FMT == F_INT) {
+            float t = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) t += __uint_as_float(w[i] << 16) + __uint_as_float(w[i] & 0xffff0000u);
+            t += __shfl_xor(t, 1, 64);
+            t += __shfl_xor(t, 2, 64);
+            if ((v & 3) == 0) xsum[r * steps * 8 + sp] = t;
+            // elements 0 4 1 5 2 6 3 7, as int4_to_bf16 orders the weights
+            w = v4u{__builtin_amdgcn_perm(w[2], w[0], 0x05040100u), __builtin_amdgcn_perm(w[2], w[0], 0x07060302u),
+                    __builtin_amdgcn_perm(w[3], w[1], 0x05040100u), __builtin_amdgcn_perm(w[3], w[1], 0x07060302u)};
+          }
+          *reinterpret_cast<v4u*>(xs + r * pitch + sp * 64 + (v & 3) * 16) = w;
+        }
+      }
+      lds_barrier();
+
+      // this lane's rows of x in operand order; the zeros stay where they are
+      const uint8_t* xl[TB];
+      int xstep[TB];
+#pragma unroll
+      for (int tb = 0; tb < TB; ++tb) {
+        const int t = DIAG ? 4 * tb + (n16 >> 2) : min(n16, rows - 1);
+        const bool live = !DIAG || ((n16 & 3) == q && t < rows);
+        xl[tb] = live ? xs + t * pitch + 128 * q : zero;
+        xstep[tb] = live ? 1 : 0;
+      }
+
+      // loads: a wave-uniform base (unit, step) plus the lane's offset
+      v4u wa[MV_DEPTH], wb[MV_DEPTH];
+      Scales<FMT, GROUP> sc[MV_DEPTH];
+      const size_t wstride = (size_t)(a.K >> 1);
+      const uint8_t *ub = nullptr, *us = nullptr, *uz = nullptr;
+      uint32_t va = 0, vb = 0, vs = 0, vz = 0;
+      auto point = [&](int cb) __attribute__((always_inline)) {
+        const int last = a.N - 1 - cb * 16;   // columns past it repeat it
+        ub = Be + (size_t)cb * 16 * wstride;
+        us = Se + (size_t)cb * 16 * sstride;
+        va = (uint32_t)min(lane >> 3, last) * (uint32_t)wstride + (lane & 7) * 16;
+        vb = (uint32_t)min((lane >> 3) + 8, last) * (uint32_t)wstride + (lane & 7) * 16;
+        vs = (uint32_t)min(n16, last) * (uint32_t)sstride + (FMT == F_MX ? 2 * q : 0);
+        if (FMT == F_INT && Ze) {
+          uz = Ze + (size_t)cb * 16 * (size_t)(a.K / GROUP);
+          vz = (uint32_t)min(n16, last) * (uint32_t)(a.K / GROUP);
+        }
+      };
+      auto load = [&](int st, int slot) __attribute__((always_inline)) {
+        const int p = min(8 * st, NP - 8);
+        const uint8_t* b = ub + (size_t)p * 16;
+        wa[slot] = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(b + va));
+        wb[slot] = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(b + vb));
+        constexpr int PG = GROUP >= 32 ? GROUP / 32 : 1;
+        const size_t g = FMT == F_MX ? p : FMT == F_NV ? 2 * p : 2 * (p / PG);
+        __builtin_memcpy(sc[slot].c, us + g + vs, Scales<FMT, GROUP>::BYTES);
+        if (FMT == F_INT && Ze) __builtin_memcpy(sc[slot].z, uz + p / PG + vz, Scales<FMT, GROUP>::NG);
+      };
+
+      v4f acc4 = {0.f, 0.f, 0.f, 0.f};
+      float acc[TB] = {};
+      const int total = nu * mine;
+      int lcb = cb0, li = 0;          // next load
+      auto load_next = [&](int slot) __attribute__((always_inline)) {
+        load(wave + MV_WAVES * li, slot);
+        if (++li == mine) {
+          li = 0;
+          if (lcb + 1 < cb0 + nu) point(++lcb);   // past the last unit: its loads once more, never used
+        }
+      };
+      // one step of the product
+      auto step = [&](int st, int slot) __attribute__((always_inline)) {
+        const int lc = lane >> 3, lp = lane & 7;
+        *reinterpret_cast<v4u*>(wbuf + lc * 128 + ((lp ^ wkey(lc)) << 4)) = wa[slot];
+        *reinterpret_cast<v4u*>(wbuf + (lc + 8) * 128 + ((lp ^ wkey(lc + 8)) << 4)) = wb[slot];
+        __builtin_amdgcn_wave_barrier();
+        v4u w[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          w[h] = *reinterpret_cast<const v4u*>(wbuf + n16 * 128 + (((2 * q + h) ^ wkey(n16)) << 4));
+        __builtin_amdgcn_wave_barrier();
+        const int off = st * (MV_STEP * 2);
+        if constexpr (FMT == F_MX) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            __builtin_amdgcn_sched_barrier(0);
+            const float s = e8m0((sc[slot].c[0] >> (8 * h)) & 0xffu);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const v4u x = *reinterpret_cast<const v4u*>(xl[0] + off + h * 64 + j * 16);
+              acc4 = mfma(x, fp4_to_bf16(w[h][j], s), acc4);
+            }
+          }
+        } else if constexpr (FMT == F_NV) {
+          float s[16];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const v2f lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)sc[slot].c[i], false);
+            const v2f hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)sc[slot].c[i], true);
+            s[4 * i] = lo[0], s[4 * i + 1] = lo[1], s[4 * i + 2] = hi[0], s[4 * i + 3] = hi[1];
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {   // 16 K: two instructions
+              __builtin_amdgcn_sched_barrier(0);
+              const v4u b0 = fp4_to_bf16(w[h][2 * g], 1.0f), b1 = fp4_to_bf16(w[h][2 * g + 1], 1.0f);
+#pragma unroll
+              for (int tb = 0; tb < TB; ++tb) {
+                const uint8_t* x = xl[tb] + (off + h * 64 + g * 32) * xstep[tb];
+                v4f p = {0.f, 0.f, 0.f, 0.f};
+                p = mfma(*reinterpret_cast<const v4u*>(x), b0, p);
+                p = mfma(*reinterpret_cast<const v4u*>(x + 16), b1, p);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[tb] = fmaf(s[4 * i + 2 * h + g], p[i], acc[tb]);
+              }
+            }
+        } else {
+          constexpr int NG = MV_STEP / GROUP, PG = 8 / NG;   // groups, pieces of a group
+          float s[NG], z[NG];
+#pragma unroll
+          for (int i = 0; i < NG; ++i) {
+            s[i] = __uint_as_float((i & 1) ? sc[slot].c[i >> 1] & 0xffff0000u : sc[slot].c[i >> 1] << 16);
+            z[i] = Ze ? -16.f - (float)((sc[slot].z[i >> 2] >> (8 * (i & 3))) & 0xffu) : -24.f;
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            v4u b[4];
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) b[j] = int4_to_bf16(w[h][j]);
+#pragma unroll
+            for (int tb = 0; tb < TB; ++tb) {
+              // the result's rows are (token 4 tb + q, piece 2i + h)
+              const float* sx = xsum + min(4 * tb + q, rows - 1) * steps * 8 + st * 8 + h;
+              v4f p;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) p[i] = z[(2 * i + h) / PG] * sx[2 * i];
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                p = mfma(*reinterpret_cast<const v4u*>(xl[tb] + (off + h * 64 + j * 16) * xstep[tb]), b[j], p);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) acc[tb] = fmaf(s[(2 * i + h) / PG], p[i], acc[tb]);
+            }
+          }
+        }
+      };
+      // end of a unit: the waves' sums join, bf16 results leave
+      auto finish = [&](int cb) __attribute__((always_inline)) {
+        float* rd = red + parity * MV_WAVES * rows_max * 16;
+        parity ^= 1;
+        if constexpr (FMT == F_MX) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (4 * q + i < rows) rd[(wave * rows_max + 4 * q + i) * 16 + n16] = acc4[i];
+          acc4 = v4f{0.f, 0.f, 0.f, 0.f};
+        } else {
+#pragma unroll
+          for (int tb = 0; tb < TB; ++tb) {
+            if (4 * tb + q < rows) rd[(wave * rows_max + 4 * tb + q) * 16 + n16] = acc[tb];
+            acc[tb] = 0.f;
+          }
+        }
+        lds_barrier();
+        const int t = tid >> 4, n = cb * 16 + (tid & 15);
+        if (t < rows && n < a.N) {
+          float v = 0.f;
+#pragma unroll
+          for (int w = 0; w < MV_WAVES; ++w) v += rd[(w * rows_max + t) * 16 + (tid & 15)];
+          a.y[(size_t)slots[t] * a.N + n] = __builtin_bit_cast(uint16_t, (__bf16)(v * gs));
+        }
+      };
+
+      if (total > 0) {
+        point(lcb);
+#pragma unroll
+        for (int i = 0; i < MV_DEPTH - 1; ++i) load_next(i);
+      }
+      if (mine == 0) {
+        for (int c = 0; c < nu; ++c) finish(cb0 + c);
+      } else {
+        int cb = cb0, i = 0;
+        for (int t = 0; t < total; t += MV_DEPTH) {
+#pragma unroll
+          for (int k = 0; k < MV_DEPTH; ++k) {
+            if (t + k < total) {
+              load_next((k + MV_DEPTH - 1) % MV_DEPTH);
+              step(wave + MV_WAVES * i, k);
+              if (++i == mine) {
+                i = 0;
+                finish(cb++);
+              }
+            }
+          }
+        }
+      }
+    }
+    u += nu;
+  }
+}
+
+constexpr int MV_LDS = 160 * 1024;   // of a CU
+
+template <int FMT, int GROUP, int TB>
+hipError_t launch_path(const MatvecArgs& a, int rows, int grid, hipStream_t stream) {
+  const int lds = mv_lds_bytes((a.K + MV_STEP - 1) / MV_STEP, rows);
+  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&matvec_kernel<FMT, GROUP, TB>),
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((matvec_kernel<FMT, GROUP, TB>), dim3(grid), dim3(MV_THREADS), lds, stream, a, rows);
+  return hipGetLastError();
+}
+
+template <int FMT, int GROUP>
+hipError_t launch_sets(const MatvecArgs& a, int rows, int grid, hipStream_t stream) {
+  if (FMT == F_MX || rows <= 4) return launch_path<FMT, GROUP, 1>(a, rows, grid, stream);
+  if (rows <= 8) return launch_path<FMT, GROUP, FMT == F_MX ? 1 : 2>(a, rows, grid, stream);
+  return launch_path<FMT, GROUP, FMT == F_MX ? 1 : 4>(a, rows, grid, stream);
 }
 
 }  // namespace
 
-hipError_t launch_matvec(const MatvecArgs& a, hipStream_t stream) {
-  const dim3 grid((a.N + 3) / 4, a.S), block(256);
-  const int per_row = a.S / a.X;
-  if (a.fmt == 0)
-    hipLaunchKernelGGL(matvec_kernel<0>, grid, block, 0, stream, a.x, per_row, a.B, a.SB, 32, a.zeros, a.gs, a.ids,
-                       a.E, a.N, a.K, a.y);
-  else if (a.fmt == 1)
-    hipLaunchKernelGGL(matvec_kernel<1>, grid, block, 0, stream, a.x, per_row, a.B, a.SB, 16, a.zeros, a.gs, a.ids,
-                       a.E, a.N, a.K, a.y);
-  else
-    hipLaunchKernelGGL(matvec_kernel<2>, grid, block, 0, stream, a.x, per_row, a.B, a.SB, a.group, a.zeros, a.gs,
-                       a.ids, a.E, a.N, a.K, a.y);
-  return hipGetLastError();
+hipError_t launch_matvec(const MatvecArgs& a, int cus, hipStream_t stream) {
+  const int steps = (a.K + MV_STEP - 1) / MV_STEP;
+  if (a.K < MV_STEP || mv_lds_bytes(steps, 1) > MV_LDS) {
+    const dim3 grid((a.N + 3) / 4, a.S), block(256);
+    if (a.fmt == F_MX) hipLaunchKernelGGL(matvec_plain_kernel<F_MX>, grid, block, 0, stream, a);
+    else if (a.fmt == F_NV) hipLaunchKernelGGL(matvec_plain_kernel<F_NV>, grid, block, 0, stream, a);
+    else hipLaunchKernelGGL(matvec_plain_kernel<F_INT>, grid, block, 0, stream, a);
+    return hipGetLastError();
+  }
+  // as many workgroups per CU as there are units for, at most four; the rows
+  // of a pass are then as many as their share of the LDS holds
+  const int64_t units = (int64_t)std::min(a.S, a.E) * ((a.N + 15) / 16);
+  int per_cu = (int)std::min<int64_t>(4, std::max<int64_t>(1, (units + cus - 1) / cus));
+  while (per_cu > 1 && mv_lds_bytes(steps, 1) > MV_LDS / per_cu) --per_cu;
+  int rows = std::min(a.S, 16);
+  while (rows > 1 && mv_lds_bytes(steps, rows) > MV_LDS / per_cu) --rows;
+  const int grid = (int)std::min<int64_t>(units, (int64_t)per_cu * cus);
+  if (a.fmt == F_MX) return launch_sets<F_MX, 32>(a, rows, grid, stream);
+  if (a.fmt == F_NV) return launch_sets<F_NV, 16>(a, rows, grid, stream);
+  if (a.group == 32) return launch_sets<F_INT, 32>(a, rows, grid, stream);
+  if (a.group == 64) return launch_sets<F_INT, 64>(a, rows, grid, stream);
+  return launch_sets<F_INT, 128>(a, rows, grid, stream);
 }
 
 }  // namespace w4a8

@@ -73,7 +73,7 @@ struct MatvecArgs {
   uint16_t* y;             // [S][N] bf16
   int X, S, E, N, K, fmt, group;
 };
-hipError_t launch_matvec(const MatvecArgs& args, hipStream_t stream);
+hipError_t launch_matvec(const MatvecArgs& args, int cus, hipStream_t stream);
 hipError_t launch_swiglu(const uint16_t* C, int R, int I, uint16_t* h, uint8_t* codes, float* scales,
                          hipStream_t stream);
 hipError_t launch_swiglu_backward(const uint8_t* codes, const float* scales, const uint16_t* dh, int R, int I,
