@@ -60,7 +60,7 @@ matvec_plain_kernel(const MatvecArgs a) {
   float acc = 0.f;
   if (e >= 0 && e < a.E) {
     const size_t col = (size_t)e * a.N + n;
-    const uint16_t* xr = a.x + (size_t)(s / (a.S / a.X)) * a.K;
+    const uint16_t* xr = a.x + (size_t)((s * a.per_row_inv) >> 16) * a.K;
     const uint32_t* w = reinterpret_cast<const uint32_t*>(a.B + col * (size_t)(a.K >> 1));
     for (int c = lane; c < a.K / 8; c += 64) {  // 8 weights: inside one group
       const size_t gi = col * (size_t)(a.K / a.group) + (8 * c) / a.group;
@@ -109,18 +109,20 @@ matvec_plain_kernel(const MatvecArgs a) {
 // is no multiple of 256 the last step starts at K - 256: what it repeats
 // meets zeros in x.
 // ---------------------------------------------------------------------------
-constexpr int MV_THREADS = 256;
-constexpr int MV_WAVES = 4;
 constexpr int MV_STEP = 256;              // K per step of a wave
 constexpr int MV_WBUF = 2048;             // a wave's LDS for one step of weights
-constexpr int MV_DEPTH = 3;               // steps of weights in registers
 constexpr int MV_X_PAD = 16;              // rows of x start 16 bytes apart modulo 256
 
 // bytes of LDS: weights, partial sums (two units), zeros, slots, x, sums of x
 __host__ __device__ inline int mv_row_bytes(int steps) { return steps * (MV_STEP * 2) + MV_X_PAD; }
-__host__ __device__ inline int mv_lds_bytes(int steps, int rows) {
-  return MV_WAVES * MV_WBUF + 2 * MV_WAVES * rows * 16 * 4 + 64 + 64 * 4 + rows * (mv_row_bytes(steps) + steps * 32);
+__host__ __device__ inline int mv_lds_bytes(int waves, int steps, int rows) {
+  return waves * MV_WBUF + 2 * waves * rows * 16 * 4 + 128 + 64 * 4 + rows * (mv_row_bytes(steps) + steps * 32);
 }
+
+// Workgroups that the registers leave room for on a CU, and the steps of
+// weights that a wave holds in registers.
+__host__ __device__ constexpr int mv_per_cu(int waves, int tb) { return waves == 8 ? 1 : tb == 4 ? 2 : 3; }
+__host__ __device__ constexpr int mv_depth(int waves) { return waves == 8 ? 4 : 3; }
 
 // Scale data of one step: MXFP4 the codes of the lane's two pieces, NVFP4 the
 // column's sixteen codes, INT4 its 256 / GROUP bf16 scales and zero points
@@ -136,12 +138,14 @@ struct Scales {
 __device__ __forceinline__ int wkey(int c) { return (c >> 1) & 7; }
 
 // 8 INT4 codes -> 16 + q as bf16, in the order 0 4 1 5 2 6 3 7
-__device__ __forceinline__ v4u int4_to_bf16(uint32_t w) {
+// (nib = 0x00780078 in a scalar register, one16 = 0x41804180 in a vector
+// register: two instructions per pair)
+__device__ __forceinline__ v4u int4_to_bf16(uint32_t w, uint32_t nib, uint32_t one16) {
   v4u o;
-  o[0] = ((w << 3) & 0x00780078u) | 0x41804180u;
-  o[1] = ((w >> 1) & 0x00780078u) | 0x41804180u;
-  o[2] = ((w >> 5) & 0x00780078u) | 0x41804180u;
-  o[3] = ((w >> 9) & 0x00780078u) | 0x41804180u;
+  o[0] = ((w << 3) & nib) | one16;
+  o[1] = ((w >> 1) & nib) | one16;
+  o[2] = ((w >> 5) & nib) | one16;
+  o[3] = ((w >> 9) & nib) | one16;
   return o;
 }
 __device__ __forceinline__ v4u fp4_to_bf16(uint32_t w, float s) {
@@ -159,6 +163,19 @@ __device__ __forceinline__ v4f mfma(v4u x, v4u w, v4f c) {
 // LDS only: every wave's LDS work done, global loads left in flight
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
+// 16 bytes per lane from src to LDS at to + 16 * lane (`to` wave-uniform).
+// Asm, because for a direct-to-LDS load that the compiler knows of it drains
+// every load in flight before the next LDS access; wait_loads waits for it.
+__device__ __forceinline__ void load_to_lds(const void* src, uint8_t* to) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src),
+               "s"(__builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)to))
+               : "memory", "m0");
+}
+
+// at most N of this wave's loads in flight (they complete in issue order)
+template <int N>
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
+
 // position of the i-th set bit of m (i below its number of set bits)
 __device__ __forceinline__ int nth_bit(uint64_t m, int i) {
   for (; i > 0; --i) m &= m - 1;
@@ -166,9 +183,10 @@ __device__ __forceinline__ int nth_bit(uint64_t m, int i) {
 }
 
 // TB: sets of four tokens (MXFP4: one set of sixteen, TB = 1).
-template <int FMT, int GROUP, int TB>
-__global__ void __launch_bounds__(MV_THREADS, 4)
+template <int FMT, int GROUP, int TB, int MV_WAVES>
+__global__ void __launch_bounds__(64 * MV_WAVES, mv_per_cu(MV_WAVES, TB) * MV_WAVES / 4)
 matvec_kernel(const MatvecArgs a, int rows_max) {
+  constexpr int MV_THREADS = 64 * MV_WAVES, MV_DEPTH = mv_depth(MV_WAVES);
   constexpr bool DIAG = FMT != F_MX;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -180,22 +198,28 @@ matvec_kernel(const MatvecArgs a, int rows_max) {
   uint8_t* wbuf = lds + wave * MV_WBUF;
   float* red = reinterpret_cast<float*>(lds + MV_WAVES * MV_WBUF);
   uint8_t* zero = reinterpret_cast<uint8_t*>(red + 2 * MV_WAVES * rows_max * 16);
-  int* slots = reinterpret_cast<int*>(zero + 64);
+  int* slots = reinterpret_cast<int*>(zero + 128);
   uint8_t* xs = reinterpret_cast<uint8_t*>(slots + 64);
   float* xsum = reinterpret_cast<float*>(xs + rows_max * pitch);   // [row][steps * 8]
-  if (tid < 16) reinterpret_cast<uint32_t*>(zero)[tid] = 0u;
+  if (tid < 32) reinterpret_cast<uint32_t*>(zero)[tid] = 0u;
 
-  // the experts that some slot names, in the order of their first slots
-  int id = lane < a.S ? (a.ids ? a.ids[lane] : 0) : -1;
-  if (id >= a.E) id = -1;
-  bool first = id >= 0;
-  for (int i = 0; i < a.S; ++i)
-    if (__builtin_amdgcn_readlane(id, i) == id && i < lane) first = false;
-  const uint64_t leaders = __ballot(first);
+  // the experts that some slot names, in the order of their first slots:
+  // `same` = the slots with this lane's expert, by one ballot per bit of the id
+  int id = 0;
+  if (a.ids) {
+    id = lane < a.S ? a.ids[lane] : -1;
+    if (id >= a.E) id = -1;
+  } else if (lane >= a.S) {
+    id = -1;
+  }
+  uint64_t same = __ballot(id >= 0);
+  for (int bit = 1; bit < a.E; bit <<= 1) {
+    const uint64_t set = __ballot(id & bit);
+    same &= (id & bit) ? set : ~set;
+  }
+  const uint64_t leaders = __ballot(id >= 0 && (same & ((1ull << lane) - 1)) == 0);
   const int D = __popcll(leaders);
   const int UB = (a.N + 15) >> 4;                     // units of an expert
-  const int64_t U = (int64_t)D * UB;
-  const int64_t u0 = U * blockIdx.x / gridDim.x, u1 = U * (blockIdx.x + 1) / gridDim.x;
 
   // slots without an expert: zeros
   for (uint64_t m = __ballot(lane < a.S && id < 0); m; m &= m - 1) {
@@ -204,16 +228,22 @@ matvec_kernel(const MatvecArgs a, int rows_max) {
       a.y[(size_t)s * a.N + n] = 0;
   }
 
-  const int per_row = a.S / a.X;
+  uint32_t nib = 0x00780078u, one16 = 0x41804180u;
+  asm volatile("" : "+s"(nib), "+v"(one16));
   int parity = 0;
-  for (int64_t u = u0; u < u1;) {
-    const int d = (int)(u / UB);
-    const int cb0 = (int)(u - (int64_t)d * UB);
-    const int nu = (int)min((int64_t)(UB - cb0), u1 - u);   // units of this expert here
+  // every expert has an equal number of workgroups, a workgroup one expert and
+  // a run of its units
+  const uint32_t each = D ? gridDim.x / (uint32_t)D : 1u;
+  const uint32_t d = blockIdx.x / each, w0 = blockIdx.x - d * each;
+  if (d < (uint32_t)D) {
+    const uint32_t share = UB / each, more = UB % each;
+    const int cb0 = share * w0 + min(w0, more);
+    const int nu = share + (w0 < more ? 1u : 0u);
     const int leader = nth_bit(leaders, d);
     const int e = __builtin_amdgcn_readlane(id, leader);
-    const uint64_t members = __ballot(id == e);
-    const int M = __popcll(members);
+    const uint64_t members = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)same, leader) |
+                             (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(same >> 32), leader) << 32;
+    const int M = nu > 0 ? __popcll(members) : 0;
     const float gs = a.gs ? a.gs[e] : 1.0f;
     const uint8_t* Be = a.B + (size_t)e * a.N * (size_t)(a.K >> 1);
     const size_t sstride = (size_t)(a.K / GROUP) * (FMT == F_INT ? 2 : 1);   // scale bytes of a column
@@ -223,45 +253,59 @@ matvec_kernel(const MatvecArgs a, int rows_max) {
     for (int r0 = 0; r0 < M; r0 += rows_max) {
       const int rows = min(rows_max, M - r0);
       lds_barrier();   // the previous pass's x and slots are no longer read
-      if (wave == 0) {
+      {  // every wave writes the same list
         const int rank = __popcll(members & ((1ull << lane) - 1)) - r0;
         if (((members >> lane) & 1) && rank >= 0 && rank < rows) slots[rank] = lane;
       }
-      // x: rows of steps * 8 pieces of 64 bytes, four lanes per piece
-      const int units16 = steps * 32;
-      for (int r = 0; r < rows; ++r) {
-        const int s = nth_bit(members, r0 + r);
-        const uint16_t* xr = a.x + (size_t)(s / per_row) * a.K;
-        for (int v = tid; v < units16; v += MV_THREADS) {
-          const int sp = v >> 2, st = sp >> 3;
-          const int p = min(8 * st, NP - 8) + (sp & 7);
-          v4u w = {0u, 0u, 0u, 0u};
-          if (p >= 8 * st) w = *reinterpret_cast<const v4u*>(xr + (size_t)p * 32 + (v & 3) * 8);
-          if (FMT == F_INT) {
+      // x into LDS without a register between: 16 bytes per lane, 64 units in a
+      // row per instruction; what the last step repeats is zeroed
+      const int per_x = steps * 32, turns = (per_x + MV_THREADS - 1) / MV_THREADS;
+      uint64_t left = members;
+      for (int i = 0; i < r0; ++i) left &= left - 1;
+      for (int r = 0; r < rows; ++r, left &= left - 1) {
+        const int slot = __ffsll((unsigned long long)left) - 1;
+        const uint16_t* xr = a.x + (size_t)((slot * a.per_row_inv) >> 16) * a.K;
+        for (int t = 0; t < turns; ++t) {
+          const int v = tid + t * MV_THREADS, st = v >> 5;
+          const int p = min(8 * st, NP - 8) + ((v >> 2) & 7);
+          uint8_t* to = xs + r * pitch + (t * MV_THREADS + wave * 64) * 16;
+          if (v < per_x) {
+            if (p >= 8 * st)
+              load_to_lds(xr + p * 32 + (v & 3) * 8, to);
+            else
+              *reinterpret_cast<v4u*>(to + lane * 16) = v4u{0u, 0u, 0u, 0u};
+          }
+        }
+      }
+      // INT4: each unit's elements in the order 0 4 1 5 2 6 3 7, as
+      // int4_to_bf16 has the weights, and the sum of every piece (four lanes)
+      auto x_finish = [&]() __attribute__((always_inline)) {
+        for (int r = 0; r < rows; ++r) {
+#pragma unroll 2
+          for (int v = tid; v < per_x; v += MV_THREADS) {
+            v4u* at = reinterpret_cast<v4u*>(xs + r * pitch + v * 16);
+            const v4u w = *at;
             float t = 0.f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) t += __uint_as_float(w[i] << 16) + __uint_as_float(w[i] & 0xffff0000u);
-            t += __shfl_xor(t, 1, 64);
-            t += __shfl_xor(t, 2, 64);
-            if ((v & 3) == 0) xsum[r * steps * 8 + sp] = t;
-            // elements 0 4 1 5 2 6 3 7, as int4_to_bf16 orders the weights
-            w = v4u{__builtin_amdgcn_perm(w[2], w[0], 0x05040100u), __builtin_amdgcn_perm(w[2], w[0], 0x07060302u),
-                    __builtin_amdgcn_perm(w[3], w[1], 0x05040100u), __builtin_amdgcn_perm(w[3], w[1], 0x07060302u)};
+            t += __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(t), 0xB1, 0xf, 0xf, false));  // lane ^ 1
+            t += __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(t), 0x4E, 0xf, 0xf, false));  // lane ^ 2
+            if ((v & 3) == 0) xsum[r * steps * 8 + (v >> 2)] = t;
+            *at = v4u{__builtin_amdgcn_perm(w[2], w[0], 0x05040100u), __builtin_amdgcn_perm(w[2], w[0], 0x07060302u),
+                      __builtin_amdgcn_perm(w[3], w[1], 0x05040100u), __builtin_amdgcn_perm(w[3], w[1], 0x07060302u)};
           }
-          *reinterpret_cast<v4u*>(xs + r * pitch + sp * 64 + (v & 3) * 16) = w;
         }
-      }
-      lds_barrier();
+      };
 
       // this lane's rows of x in operand order; the zeros stay where they are
       const uint8_t* xl[TB];
-      int xstep[TB];
+      bool xlive[TB];
 #pragma unroll
       for (int tb = 0; tb < TB; ++tb) {
         const int t = DIAG ? 4 * tb + (n16 >> 2) : min(n16, rows - 1);
         const bool live = !DIAG || ((n16 & 3) == q && t < rows);
         xl[tb] = live ? xs + t * pitch + 128 * q : zero;
-        xstep[tb] = live ? 1 : 0;
+        xlive[tb] = live;
       }
 
       // loads: a wave-uniform base (unit, step) plus the lane's offset
@@ -277,20 +321,20 @@ matvec_kernel(const MatvecArgs a, int rows_max) {
         va = (uint32_t)min(lane >> 3, last) * (uint32_t)wstride + (lane & 7) * 16;
         vb = (uint32_t)min((lane >> 3) + 8, last) * (uint32_t)wstride + (lane & 7) * 16;
         vs = (uint32_t)min(n16, last) * (uint32_t)sstride + (FMT == F_MX ? 2 * q : 0);
-        if (FMT == F_INT && Ze) {
-          uz = Ze + (size_t)cb * 16 * (size_t)(a.K / GROUP);
+        if (FMT == F_INT) {   // without zero points the loads read scales, unused
+          uz = Ze ? Ze + (size_t)cb * 16 * (size_t)(a.K / GROUP) : us;
           vz = (uint32_t)min(n16, last) * (uint32_t)(a.K / GROUP);
         }
       };
       auto load = [&](int st, int slot) __attribute__((always_inline)) {
-        const int p = min(8 * st, NP - 8);
+        const int p = min(8 * st, NP - 8);   // a wave without steps reads the last one, unused
         const uint8_t* b = ub + (size_t)p * 16;
         wa[slot] = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(b + va));
         wb[slot] = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(b + vb));
         constexpr int PG = GROUP >= 32 ? GROUP / 32 : 1;
         const size_t g = FMT == F_MX ? p : FMT == F_NV ? 2 * p : 2 * (p / PG);
         __builtin_memcpy(sc[slot].c, us + g + vs, Scales<FMT, GROUP>::BYTES);
-        if (FMT == F_INT && Ze) __builtin_memcpy(sc[slot].z, uz + p / PG + vz, Scales<FMT, GROUP>::NG);
+        if (FMT == F_INT) __builtin_memcpy(sc[slot].z, uz + p / PG + vz, Scales<FMT, GROUP>::NG);
       };
 
       v4f acc4 = {0.f, 0.f, 0.f, 0.f};
@@ -315,17 +359,21 @@ matvec_kernel(const MatvecArgs a, int rows_max) {
         for (int h = 0; h < 2; ++h)
           w[h] = *reinterpret_cast<const v4u*>(wbuf + n16 * 128 + (((2 * q + h) ^ wkey(n16)) << 4));
         __builtin_amdgcn_wave_barrier();
-        const int off = st * (MV_STEP * 2);
+        const uint8_t* x[TB];   // of this step: 128 bytes, h * 64 + j * 16
+#pragma unroll
+        for (int tb = 0; tb < TB; ++tb) x[tb] = xl[tb] + (xlive[tb] ? st * (MV_STEP * 2) : 0);
+        auto frag = [&](int tb, int at) __attribute__((always_inline)) {
+          return *reinterpret_cast<const v4u*>(x[tb] + at);
+        };
         if constexpr (FMT == F_MX) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            __builtin_amdgcn_sched_barrier(0);
+            v4u xf[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) xf[j] = frag(0, h * 64 + j * 16);
             const float s = e8m0((sc[slot].c[0] >> (8 * h)) & 0xffu);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const v4u x = *reinterpret_cast<const v4u*>(xl[0] + off + h * 64 + j * 16);
-              acc4 = mfma(x, fp4_to_bf16(w[h][j], s), acc4);
-            }
+            for (int j = 0; j < 4; ++j) acc4 = mfma(xf[j], fp4_to_bf16(w[h][j], s), acc4);
           }
         } else if constexpr (FMT == F_NV) {
           float s[16];
@@ -336,21 +384,26 @@ matvec_kernel(const MatvecArgs a, int rows_max) {
             s[4 * i] = lo[0], s[4 * i + 1] = lo[1], s[4 * i + 2] = hi[0], s[4 * i + 3] = hi[1];
           }
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+          for (int h = 0; h < 2; ++h) {
+            __builtin_amdgcn_sched_barrier(0);   // one piece's operands at a time
+            v4u b[4];
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {   // 16 K: two instructions
-              __builtin_amdgcn_sched_barrier(0);
-              const v4u b0 = fp4_to_bf16(w[h][2 * g], 1.0f), b1 = fp4_to_bf16(w[h][2 * g + 1], 1.0f);
+            for (int j = 0; j < 4; ++j) b[j] = fp4_to_bf16(w[h][j], 1.0f);
 #pragma unroll
-              for (int tb = 0; tb < TB; ++tb) {
-                const uint8_t* x = xl[tb] + (off + h * 64 + g * 32) * xstep[tb];
+            for (int tb = 0; tb < TB; ++tb) {
+              v4u xf[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) xf[j] = frag(tb, h * 64 + j * 16);
+#pragma unroll
+              for (int g = 0; g < 2; ++g) {   // 16 K: two instructions
                 v4f p = {0.f, 0.f, 0.f, 0.f};
-                p = mfma(*reinterpret_cast<const v4u*>(x), b0, p);
-                p = mfma(*reinterpret_cast<const v4u*>(x + 16), b1, p);
+                p = mfma(xf[2 * g], b[2 * g], p);
+                p = mfma(xf[2 * g + 1], b[2 * g + 1], p);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[tb] = fmaf(s[4 * i + 2 * h + g], p[i], acc[tb]);
               }
             }
+          }
         } else {
           constexpr int NG = MV_STEP / GROUP, PG = 8 / NG;   // groups, pieces of a group
           float s[NG], z[NG];
@@ -361,20 +414,22 @@ matvec_kernel(const MatvecArgs a, int rows_max) {
           }
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
+            __builtin_amdgcn_sched_barrier(0);   // one piece's operands at a time
             v4u b[4];
-            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) b[j] = int4_to_bf16(w[h][j]);
+            for (int j = 0; j < 4; ++j) b[j] = int4_to_bf16(w[h][j], nib, one16);
 #pragma unroll
             for (int tb = 0; tb < TB; ++tb) {
               // the result's rows are (token 4 tb + q, piece 2i + h)
               const float* sx = xsum + min(4 * tb + q, rows - 1) * steps * 8 + st * 8 + h;
+              v4u xf[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) xf[j] = frag(tb, h * 64 + j * 16);
               v4f p;
 #pragma unroll
               for (int i = 0; i < 4; ++i) p[i] = z[(2 * i + h) / PG] * sx[2 * i];
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                p = mfma(*reinterpret_cast<const v4u*>(xl[tb] + (off + h * 64 + j * 16) * xstep[tb]), b[j], p);
+              for (int j = 0; j < 4; ++j) p = mfma(xf[j], b[j], p);
 #pragma unroll
               for (int i = 0; i < 4; ++i) acc[tb] = fmaf(s[(2 * i + h) / PG], p[i], acc[tb]);
             }
@@ -407,23 +462,29 @@ matvec_kernel(const MatvecArgs a, int rows_max) {
         }
       };
 
-      if (total > 0) {
-        point(lcb);
+      // the first weights behind x; then this wave's part of x has landed once
+      // no more than those are in flight
+      point(lcb);
 #pragma unroll
-        for (int i = 0; i < MV_DEPTH - 1; ++i) load_next(i);
-      }
+      for (int k = 0; k < MV_DEPTH - 1; ++k) load_next(k);
+      wait_loads<3 * (MV_DEPTH - 1)>();
+      if constexpr (FMT == F_INT) x_finish();
+      lds_barrier();
+
       if (mine == 0) {
         for (int c = 0; c < nu; ++c) finish(cb0 + c);
       } else {
-        int cb = cb0, i = 0;
+        int cb = cb0, si = 0;
         for (int t = 0; t < total; t += MV_DEPTH) {
 #pragma unroll
           for (int k = 0; k < MV_DEPTH; ++k) {
+            // loads in every turn, so that each wait is one constant: past the
+            // end they read the last unit again
+            load_next((k + MV_DEPTH - 1) % MV_DEPTH);
             if (t + k < total) {
-              load_next((k + MV_DEPTH - 1) % MV_DEPTH);
-              step(wave + MV_WAVES * i, k);
-              if (++i == mine) {
-                i = 0;
+              step(wave + MV_WAVES * si, k);
+              if (++si == mine) {
+                si = 0;
                 finish(cb++);
               }
             }
@@ -431,53 +492,67 @@ matvec_kernel(const MatvecArgs a, int rows_max) {
         }
       }
     }
-    u += nu;
   }
 }
 
 constexpr int MV_LDS = 160 * 1024;   // of a CU
 
-template <int FMT, int GROUP, int TB>
-hipError_t launch_path(const MatvecArgs& a, int rows, int grid, hipStream_t stream) {
-  const int lds = mv_lds_bytes((a.K + MV_STEP - 1) / MV_STEP, rows);
-  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&matvec_kernel<FMT, GROUP, TB>),
+template <int FMT, int GROUP, int TB, int WAVES>
+hipError_t launch_path(const MatvecArgs& a, int rows, int grid, int lds, hipStream_t stream) {
+  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&matvec_kernel<FMT, GROUP, TB, WAVES>),
                                            hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((matvec_kernel<FMT, GROUP, TB>), dim3(grid), dim3(MV_THREADS), lds, stream, a, rows);
+  hipLaunchKernelGGL((matvec_kernel<FMT, GROUP, TB, WAVES>), dim3(grid), dim3(64 * WAVES), lds, stream, a, rows);
   return hipGetLastError();
 }
 
-template <int FMT, int GROUP>
-hipError_t launch_sets(const MatvecArgs& a, int rows, int grid, hipStream_t stream) {
-  if (FMT == F_MX || rows <= 4) return launch_path<FMT, GROUP, 1>(a, rows, grid, stream);
-  if (rows <= 8) return launch_path<FMT, GROUP, FMT == F_MX ? 1 : 2>(a, rows, grid, stream);
-  return launch_path<FMT, GROUP, FMT == F_MX ? 1 : 4>(a, rows, grid, stream);
+template <int FMT, int GROUP, int WAVES>
+hipError_t launch_sets(const MatvecArgs& a, int rows, int grid, int lds, hipStream_t stream) {
+  if (FMT == F_MX || rows <= 4) return launch_path<FMT, GROUP, 1, WAVES>(a, rows, grid, lds, stream);
+  if (rows <= 8) return launch_path<FMT, GROUP, FMT == F_MX ? 1 : 2, WAVES>(a, rows, grid, lds, stream);
+  return launch_path<FMT, GROUP, FMT == F_MX ? 1 : 4, WAVES>(a, rows, grid, lds, stream);
+}
+
+template <int WAVES>
+hipError_t launch_waves(const MatvecArgs& a, int cus, int64_t units, hipStream_t stream) {
+  // rows of a pass: all of a dense call's, twice the mean of an expert's (at
+  // least four), as far as the LDS holds them; then as many workgroups per CU
+  // as there are units, registers and LDS for
+  const int steps = (a.K + MV_STEP - 1) / MV_STEP;
+  int rows = std::min(std::min(a.S, 16), a.ids ? std::max(4, 2 * ((a.S + a.E - 1) / a.E)) : 16);
+  int per_cu = (int)std::min<int64_t>(mv_per_cu(WAVES, a.fmt != F_MX && rows > 8 ? 4 : 1),
+                                      std::max<int64_t>(1, (units + cus - 1) / cus));
+  while (per_cu > 1 && mv_lds_bytes(WAVES, steps, std::min(rows, 4)) > MV_LDS / per_cu) --per_cu;
+  while (rows > 1 && mv_lds_bytes(WAVES, steps, rows) > MV_LDS / per_cu) --rows;
+  const int grid = (int)std::min<int64_t>(units, (int64_t)per_cu * cus);
+  const int lds = mv_lds_bytes(WAVES, steps, rows);
+  if (a.fmt == F_MX) return launch_sets<F_MX, 32, WAVES>(a, rows, grid, lds, stream);
+  if (a.fmt == F_NV) return launch_sets<F_NV, 16, WAVES>(a, rows, grid, lds, stream);
+  if (a.group == 32) return launch_sets<F_INT, 32, WAVES>(a, rows, grid, lds, stream);
+  if (a.group == 64) return launch_sets<F_INT, 64, WAVES>(a, rows, grid, lds, stream);
+  return launch_sets<F_INT, 128, WAVES>(a, rows, grid, lds, stream);
 }
 
 }  // namespace
 
 hipError_t launch_matvec(const MatvecArgs& a, int cus, hipStream_t stream) {
   const int steps = (a.K + MV_STEP - 1) / MV_STEP;
-  if (a.K < MV_STEP || mv_lds_bytes(steps, 1) > MV_LDS) {
+  if (a.K < MV_STEP || mv_lds_bytes(8, steps, 1) > MV_LDS) {
     const dim3 grid((a.N + 3) / 4, a.S), block(256);
     if (a.fmt == F_MX) hipLaunchKernelGGL(matvec_plain_kernel<F_MX>, grid, block, 0, stream, a);
     else if (a.fmt == F_NV) hipLaunchKernelGGL(matvec_plain_kernel<F_NV>, grid, block, 0, stream, a);
     else hipLaunchKernelGGL(matvec_plain_kernel<F_INT>, grid, block, 0, stream, a);
     return hipGetLastError();
   }
-  // as many workgroups per CU as there are units for, at most four; the rows
-  // of a pass are then as many as their share of the LDS holds
+  // Eight waves where a CU gets one workgroup in any case: not enough units
+  // for two (INT4, 5 rows of 6144 x 3583: 12.0 against 13.3 us with four), or
+  // so many rows of x that the LDS holds no second (16 rows of 6144 x 6144,
+  // MXFP4: 16.8 against 23.9 us, NVFP4: 22.9 against 26.5).  Else four (one
+  // token of 8 experts 4096 x 6144, INT4: 21.7 against 22.5 us; 24 slots of
+  // 6144 x 2048, NVFP4: 25.8 against 27.4).
   const int64_t units = (int64_t)std::min(a.S, a.E) * ((a.N + 15) / 16);
-  int per_cu = (int)std::min<int64_t>(4, std::max<int64_t>(1, (units + cus - 1) / cus));
-  while (per_cu > 1 && mv_lds_bytes(steps, 1) > MV_LDS / per_cu) --per_cu;
-  int rows = std::min(a.S, 16);
-  while (rows > 1 && mv_lds_bytes(steps, rows) > MV_LDS / per_cu) --rows;
-  const int grid = (int)std::min<int64_t>(units, (int64_t)per_cu * cus);
-  if (a.fmt == F_MX) return launch_sets<F_MX, 32>(a, rows, grid, stream);
-  if (a.fmt == F_NV) return launch_sets<F_NV, 16>(a, rows, grid, stream);
-  if (a.group == 32) return launch_sets<F_INT, 32>(a, rows, grid, stream);
-  if (a.group == 64) return launch_sets<F_INT, 64>(a, rows, grid, stream);
-  return launch_sets<F_INT, 128>(a, rows, grid, stream);
+  if (units <= cus || (!a.ids && a.S > 8)) return launch_waves<8>(a, cus, units, stream);
+  return launch_waves<4>(a, cus, units, stream);
 }
 
 }  // namespace w4a8

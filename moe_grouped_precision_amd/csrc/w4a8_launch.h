@@ -71,7 +71,8 @@ struct MatvecArgs {
   const float* gs;         // [E] or null
   const int32_t* ids;      // [S] or null (E = 1)
   uint16_t* y;             // [S][N] bf16
-  int X, S, E, N, K, fmt, group;
+  int S, E, N, K, fmt, group;
+  int per_row_inv;         // slot s multiplies row (s * per_row_inv) >> 16 of x (s < 64)
 };
 hipError_t launch_matvec(const MatvecArgs& args, int cus, hipStream_t stream);
 hipError_t launch_swiglu(const uint16_t* C, int R, int I, uint16_t* h, uint8_t* codes, float* scales,
