@@ -25,7 +25,8 @@ typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 constexpr float kCkptFloor = 7.888609052210118e-31f;  // 2^-100
 
 __device__ __forceinline__ void load16(const uint16_t* p, float (&f)[16]) {
-  const v4u a = *reinterpret_cast<const v4u*>(p), b = *(reinterpret_cast<const v4u*>(p) + 1);
+  const v4u a = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(p));
+  const v4u b = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(p) + 1);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     f[2 * i] = __uint_as_float(a[i] << 16);
@@ -41,8 +42,8 @@ __device__ __forceinline__ void store16(uint16_t* p, const float (&f)[16]) {
     a[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f){f[2 * i], f[2 * i + 1]}, v2bf));
     b[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f){f[8 + 2 * i], f[8 + 2 * i + 1]}, v2bf));
   }
-  *reinterpret_cast<v4u*>(p) = a;
-  *(reinterpret_cast<v4u*>(p) + 1) = b;
+  __builtin_nontemporal_store(a, reinterpret_cast<v4u*>(p));
+  __builtin_nontemporal_store(b, reinterpret_cast<v4u*>(p) + 1);
 }
 
 // The 8-bit copy of one lane's 16 columns; the group's 8 lanes agree on the
@@ -65,7 +66,7 @@ __device__ __forceinline__ void quant16(const float (&f)[16], uint8_t* codes, fl
     w = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * i + 2] * inv, f[4 * i + 3] * inv, w, true);
     c[i] = (uint32_t)w;
   }
-  *reinterpret_cast<v4u*>(codes) = c;
+  __builtin_nontemporal_store(c, reinterpret_cast<v4u*>(codes));
   if (write_scale) *scale = q;
 }
 
@@ -93,7 +94,7 @@ swiglu_kernel(const uint16_t* __restrict__ C, int64_t groups, int I, uint16_t* _
 }
 
 __device__ __forceinline__ void decode16(const uint8_t* p, float (&f)[16]) {
-  const v4u c = *reinterpret_cast<const v4u*>(p);
+  const v4u c = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(p));
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const v2f a = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[i], false), b = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[i], true);
