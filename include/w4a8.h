@@ -530,7 +530,8 @@ int w4a8_matvec(const uint16_t* x_bf16_dev, int X, const uint8_t* B_dev, const v
  * code = E4M3FN round-to-nearest-even of C * (1/s), fp32 divisions rounded
  * to nearest: the copy's bits are unique.  NaN keeps a NaN code; a group
  * with an infinity gets an infinite scale and reads back as NaN.
- * Limits: R >= 0, I % 128 == 0, 128 <= I <= W4A8_MAX_K, R * I/128 < 2^36.
+ * Limits: R >= 0, I % 128 == 0, 128 <= I <= W4A8_MAX_K, R * ceil(I/2048) <
+ * 2^31.
  * R == 0 does nothing.  16-byte alignment except for the scales.
  */
 int w4a8_swiglu(const uint16_t* C_bf16_dev, int R, int I, uint16_t* h_bf16_dev, uint8_t* ckpt_fp8_dev,

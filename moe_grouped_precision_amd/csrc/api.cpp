@@ -546,7 +546,7 @@ int w4a8_swiglu(const uint16_t* C_bf16_dev, int R, int I, uint16_t* h_bf16_dev, 
   if (R < 0) return fail(W4A8_ERR_SHAPE, "R=%d", R);
   if (I < 128 || I % 128 || I > W4A8_MAX_K)
     return fail(W4A8_ERR_SHAPE, "I=%d must be a multiple of 128 in [128, %d]", I, W4A8_MAX_K);
-  if ((int64_t)R * (I / 128) >= (int64_t)1 << 36) return fail(W4A8_ERR_SHAPE, "R * I/128 too large");
+  if ((int64_t)R * ((I + 2047) / 2048) >= (int64_t)1 << 31) return fail(W4A8_ERR_SHAPE, "R * ceil(I/2048) too large");
   if (R > 0 && (!C_bf16_dev || !h_bf16_dev)) return fail(W4A8_ERR_NULL, "null pointer argument");
   if (!ckpt_fp8_dev != !ckpt_scales_dev) return fail(W4A8_ERR_NULL, "the checkpoint's codes and scales go together");
   if (!aligned(C_bf16_dev, 16) || !aligned(h_bf16_dev, 16) || !aligned(ckpt_fp8_dev, 16) ||
@@ -567,7 +567,7 @@ int w4a8_swiglu_backward(const uint8_t* ckpt_fp8_dev, const float* ckpt_scales_d
   if (R < 0) return fail(W4A8_ERR_SHAPE, "R=%d", R);
   if (I < 128 || I % 128 || I > W4A8_MAX_K)
     return fail(W4A8_ERR_SHAPE, "I=%d must be a multiple of 128 in [128, %d]", I, W4A8_MAX_K);
-  if ((int64_t)R * (I / 128) >= (int64_t)1 << 36) return fail(W4A8_ERR_SHAPE, "R * I/128 too large");
+  if ((int64_t)R * ((I + 2047) / 2048) >= (int64_t)1 << 31) return fail(W4A8_ERR_SHAPE, "R * ceil(I/2048) too large");
   if (R > 0 && (!ckpt_fp8_dev || !ckpt_scales_dev || !dh_bf16_dev || !dC_bf16_dev))
     return fail(W4A8_ERR_NULL, "null pointer argument");
   if (!aligned(ckpt_fp8_dev, 16) || !aligned(dh_bf16_dev, 16) || !aligned(dC_bf16_dev, 16) ||

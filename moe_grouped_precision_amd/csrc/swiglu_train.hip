@@ -8,8 +8,9 @@
 //         dg = dh u s (1 + g (1 - s)),  du = dh g s,  h = g s u
 // fp32 throughout, one rounding to bf16 per output.
 //
-// A stream: 8 lanes per 128 columns of g and the same of u, 16 columns of
-// each per lane, the group maxima by three lane exchanges; no LDS, no barrier.
+// A stream: 16 lanes per 128 columns of g and the same of u, 8 columns of each
+// per lane (16-byte loads, consecutive lanes), the group maxima by DPP
+// rotations; no LDS, no barrier.
 #include "swiglu.h"
 #include "w4a8_launch.h"
 
@@ -19,84 +20,90 @@ namespace w4a8 {
 namespace {
 
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 typedef float v2f __attribute__((ext_vector_type(2)));
 typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 
 constexpr float kCkptFloor = 7.888609052210118e-31f;  // 2^-100
 
-__device__ __forceinline__ void load16(const uint16_t* p, float (&f)[16]) {
+__device__ __forceinline__ void load8(const uint16_t* p, float (&f)[8]) {
   const v4u a = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(p));
-  const v4u b = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(p) + 1);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     f[2 * i] = __uint_as_float(a[i] << 16);
     f[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
-    f[8 + 2 * i] = __uint_as_float(b[i] << 16);
-    f[8 + 2 * i + 1] = __uint_as_float(b[i] & 0xffff0000u);
   }
 }
-__device__ __forceinline__ void store16(uint16_t* p, const float (&f)[16]) {
-  v4u a, b;
+__device__ __forceinline__ void store8(uint16_t* p, const float (&f)[8]) {
+  v4u a;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 4; ++i)
     a[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f){f[2 * i], f[2 * i + 1]}, v2bf));
-    b[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f){f[8 + 2 * i], f[8 + 2 * i + 1]}, v2bf));
-  }
   __builtin_nontemporal_store(a, reinterpret_cast<v4u*>(p));
-  __builtin_nontemporal_store(b, reinterpret_cast<v4u*>(p) + 1);
 }
 
-// The 8-bit copy of one lane's 16 columns; the group's 8 lanes agree on the
+// Maximum over 16 lanes, in each of them.
+template <int CTRL>
+__device__ __forceinline__ float max_dpp(float v) {
+  return fmaxf(v, __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), CTRL, 0xf, 0xf, true)));
+}
+__device__ __forceinline__ float max16(float v) {
+  v = max_dpp<0x128>(v);   // row_ror 8, 4, 2, 1
+  v = max_dpp<0x124>(v);
+  v = max_dpp<0x122>(v);
+  return max_dpp<0x121>(v);
+}
+
+// The 8-bit copy of one lane's 8 columns; the group's 16 lanes agree on the
 // scale.  No clip: |f / q| stays under 448 (1 + 2^-8), which rounds to 448; a
 // NaN keeps its NaN code, an infinity makes the group's scale infinite and
 // the group NaN when it is read.
-__device__ __forceinline__ void quant16(const float (&f)[16], uint8_t* codes, float* scale, bool write_scale) {
+__device__ __forceinline__ void quant8(const float (&f)[8], uint8_t* codes, float* scale, bool write_scale) {
   float m = 0.f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(f[i]));
-  m = fmaxf(m, __shfl_xor(m, 1, 8));
-  m = fmaxf(m, __shfl_xor(m, 2, 8));
-  m = fmaxf(m, __shfl_xor(m, 4, 8));
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(f[i]));
+  m = max16(m);
   const float q = m < kCkptFloor ? 1.0f : __fdiv_rn(m, 448.0f);
   const float inv = __fdiv_rn(1.0f, q);
-  v4u c;
+  v2u c;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 2; ++i) {
     int w = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * i] * inv, f[4 * i + 1] * inv, 0, false);
     w = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * i + 2] * inv, f[4 * i + 3] * inv, w, true);
     c[i] = (uint32_t)w;
   }
-  __builtin_nontemporal_store(c, reinterpret_cast<v4u*>(codes));
+  __builtin_nontemporal_store(c, reinterpret_cast<v2u*>(codes));
   if (write_scale) *scale = q;
 }
 
+constexpr int S_GROUPS = 16;   // most groups of a workgroup
+
 template <bool CKPT>
-__global__ void __launch_bounds__(256)
-swiglu_kernel(const uint16_t* __restrict__ C, int64_t groups, int I, uint16_t* __restrict__ h,
+__global__ void __launch_bounds__(16 * S_GROUPS)
+swiglu_kernel(const uint16_t* __restrict__ C, int blocks, int I, uint16_t* __restrict__ h,
               uint8_t* __restrict__ codes, float* __restrict__ scales) {
   const int G = I >> 7;
-  const int lane8 = threadIdx.x & 7;
-  const int64_t i = (int64_t)blockIdx.x * 32 + (threadIdx.x >> 3);
-  if (i >= groups) return;
-  const int64_t r = i / G;
-  const int g = (int)(i - r * G);
-  const size_t at = (size_t)r * 2 * I + g * 128 + lane8 * 16;
-  float fg[16], fu[16], fh[16];
-  load16(C + at, fg);
-  load16(C + at + I, fu);
+  const int lane = threadIdx.x & 15;
+  const uint32_t r = blockIdx.x / (uint32_t)blocks;   // blocks: workgroups of a row
+  const int g = (int)(blockIdx.x - r * blocks) * (int)(blockDim.x >> 4) + (int)(threadIdx.x >> 4);
+  if (g >= G) return;
+  const size_t at = (size_t)r * 2 * I + g * 128 + lane * 8;
+  float fg[8], fu[8], fh[8];
+  load8(C + at, fg);
+  load8(C + at + I, fu);
 #pragma unroll
-  for (int e = 0; e < 16; ++e) fh[e] = swiglu_f32(fg[e], fu[e]);
-  store16(h + (size_t)r * I + g * 128 + lane8 * 16, fh);
+  for (int e = 0; e < 8; ++e) fh[e] = swiglu_f32(fg[e], fu[e]);
+  store8(h + (size_t)r * I + g * 128 + lane * 8, fh);
   if (CKPT) {
-    quant16(fg, codes + at, scales + (size_t)r * 2 * G + g, lane8 == 0);
-    quant16(fu, codes + at + I, scales + (size_t)r * 2 * G + G + g, lane8 == 0);
+    quant8(fg, codes + at, scales + (size_t)r * 2 * G + g, lane == 0);
+    quant8(fu, codes + at + I, scales + (size_t)r * 2 * G + G + g, lane == 0);
   }
 }
 
-__device__ __forceinline__ void decode16(const uint8_t* p, float (&f)[16]) {
-  const v4u c = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(p));
+__device__ __forceinline__ void decode8(const uint8_t* p, float (&f)[8]) {
+  const v2u c = __builtin_nontemporal_load(reinterpret_cast<const v2u*>(p));
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 2; ++i) {
     const v2f a = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[i], false), b = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[i], true);
     f[4 * i] = a[0];
     f[4 * i + 1] = a[1];
@@ -106,26 +113,25 @@ __device__ __forceinline__ void decode16(const uint8_t* p, float (&f)[16]) {
 }
 
 template <bool WITH_H>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(16 * S_GROUPS)
 swiglu_backward_kernel(const uint8_t* __restrict__ codes, const float* __restrict__ scales,
-                       const uint16_t* __restrict__ dh, int64_t groups, int I, uint16_t* __restrict__ dC,
+                       const uint16_t* __restrict__ dh, int blocks, int I, uint16_t* __restrict__ dC,
                        uint16_t* __restrict__ h) {
   const int G = I >> 7;
-  const int lane8 = threadIdx.x & 7;
-  const int64_t i = (int64_t)blockIdx.x * 32 + (threadIdx.x >> 3);
-  if (i >= groups) return;
-  const int64_t r = i / G;
-  const int g = (int)(i - r * G);
-  const size_t at = (size_t)r * 2 * I + g * 128 + lane8 * 16;
-  const size_t hat = (size_t)r * I + g * 128 + lane8 * 16;
-  float fg[16], fu[16], fd[16];
+  const int lane = threadIdx.x & 15;
+  const uint32_t r = blockIdx.x / (uint32_t)blocks;   // blocks: workgroups of a row
+  const int g = (int)(blockIdx.x - r * blocks) * (int)(blockDim.x >> 4) + (int)(threadIdx.x >> 4);
+  if (g >= G) return;
+  const size_t at = (size_t)r * 2 * I + g * 128 + lane * 8;
+  const size_t hat = (size_t)r * I + g * 128 + lane * 8;
+  float fg[8], fu[8], fd[8];
   const float qg = scales[(size_t)r * 2 * G + g], qu = scales[(size_t)r * 2 * G + G + g];
-  decode16(codes + at, fg);
-  decode16(codes + at + I, fu);
-  load16(dh + hat, fd);
-  float dg[16], du[16], hh[16];
+  decode8(codes + at, fg);
+  decode8(codes + at + I, fu);
+  load8(dh + hat, fd);
+  float dg[8], du[8], hh[8];
 #pragma unroll
-  for (int e = 0; e < 16; ++e) {
+  for (int e = 0; e < 8; ++e) {
     // g = code * q needs 28 bits: what fp32 cuts off it (lo) would cost |g|
     // times its size in e^-g, so e^-(g + lo) = e^-g (1 - lo).  e^-g is capped
     // at e^88, where it and its reciprocal stay finite.
@@ -138,32 +144,32 @@ swiglu_backward_kernel(const uint8_t* __restrict__ codes, const float* __restric
     du[e] = fd[e] * silu;
     hh[e] = silu * uv;
   }
-  store16(dC + at, dg);
-  store16(dC + at + I, du);
-  if (WITH_H) store16(h + hat, hh);
+  store8(dC + at, dg);
+  store8(dC + at + I, du);
+  if (WITH_H) store8(h + hat, hh);
 }
 
 }  // namespace
 
 hipError_t launch_swiglu(const uint16_t* C, int R, int I, uint16_t* h, uint8_t* codes, float* scales,
                          hipStream_t stream) {
-  const int64_t groups = (int64_t)R * (I >> 7);
-  const dim3 grid((unsigned)((groups + 31) / 32));
+  const int G = I >> 7, blocks = (G + S_GROUPS - 1) / S_GROUPS;
+  const dim3 grid((unsigned)R * (unsigned)blocks), block(16 * (G < S_GROUPS ? G : S_GROUPS));
   if (codes)
-    hipLaunchKernelGGL(swiglu_kernel<true>, grid, dim3(256), 0, stream, C, groups, I, h, codes, scales);
+    hipLaunchKernelGGL(swiglu_kernel<true>, grid, block, 0, stream, C, blocks, I, h, codes, scales);
   else
-    hipLaunchKernelGGL(swiglu_kernel<false>, grid, dim3(256), 0, stream, C, groups, I, h, codes, scales);
+    hipLaunchKernelGGL(swiglu_kernel<false>, grid, block, 0, stream, C, blocks, I, h, codes, scales);
   return hipGetLastError();
 }
 
 hipError_t launch_swiglu_backward(const uint8_t* codes, const float* scales, const uint16_t* dh, int R, int I,
                                   uint16_t* dC, uint16_t* h, hipStream_t stream) {
-  const int64_t groups = (int64_t)R * (I >> 7);
-  const dim3 grid((unsigned)((groups + 31) / 32));
+  const int G = I >> 7, blocks = (G + S_GROUPS - 1) / S_GROUPS;
+  const dim3 grid((unsigned)R * (unsigned)blocks), block(16 * (G < S_GROUPS ? G : S_GROUPS));
   if (h)
-    hipLaunchKernelGGL(swiglu_backward_kernel<true>, grid, dim3(256), 0, stream, codes, scales, dh, groups, I, dC, h);
+    hipLaunchKernelGGL(swiglu_backward_kernel<true>, grid, block, 0, stream, codes, scales, dh, blocks, I, dC, h);
   else
-    hipLaunchKernelGGL(swiglu_backward_kernel<false>, grid, dim3(256), 0, stream, codes, scales, dh, groups, I, dC, h);
+    hipLaunchKernelGGL(swiglu_backward_kernel<false>, grid, block, 0, stream, codes, scales, dh, blocks, I, dC, h);
   return hipGetLastError();
 }
 
