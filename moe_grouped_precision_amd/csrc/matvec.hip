@@ -281,7 +281,6 @@ matvec_kernel(const MatvecArgs a, int rows_max) {
       // int4_to_bf16 has the weights, and the sum of every piece (four lanes)
       auto x_finish = [&]() __attribute__((always_inline)) {
         for (int r = 0; r < rows; ++r) {
-#pragma unroll 2
           for (int v = tid; v < per_x; v += MV_THREADS) {
             v4u* at = reinterpret_cast<v4u*>(xs + r * pitch + v * 16);
             const v4u w = *at;
