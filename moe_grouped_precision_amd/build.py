@@ -53,9 +53,9 @@ def compile_flags(debug: bool = False):
     return flags
 
 
-# sources whose K loops issue inline-asm memory operations: their device
+# sources that issue inline-asm memory operations: their device
 # assembly is checked after every build (see asmcheck.py)
-ASM_CHECKED = ["gemm.hip"]
+ASM_CHECKED = ["gemm.hip", "matvec.hip"]
 
 
 def check_device_asm(cc: str, tmp: str, verbose: bool = False) -> None:

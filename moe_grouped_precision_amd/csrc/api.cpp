@@ -534,8 +534,10 @@ int w4a8_matvec(const uint16_t* x_bf16_dev, int X, const uint8_t* B_dev, const v
   int st = device_info(&d);
   if (st != W4A8_OK) return st;
   if (S == 0) return ok();
+  const uint32_t wcol = K / 2, zcol = K / group, scol = b_scale_format == W4A8_WSCALE_INT4 ? 2 * zcol : zcol;
   const w4a8::MatvecArgs args{x_bf16_dev, B_dev, b_scales_dev, zeros_dev, expert_scales_dev, expert_ids_dev,
-                              y_bf16_dev, S, E, N, K, b_scale_format, group, 65536 / (S / X) + (S > X ? 1 : 0)};
+                              y_bf16_dev, S, E, N, K, b_scale_format, group, 65536 / (S / X) + (S > X ? 1 : 0),
+                              wcol, scol, zcol, wcol * (uint32_t)N, scol * (uint32_t)N, zcol * (uint32_t)N};
   hipError_t e = w4a8::launch_matvec(args, d->cus, (hipStream_t)stream);
   if (e != hipSuccess) return fail(W4A8_ERR_HIP, "matvec launch: %s", hipGetErrorString(e));
   return ok();

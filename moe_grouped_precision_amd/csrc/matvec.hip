@@ -9,8 +9,8 @@
 //
 // Bound by the weights' bytes: every expert that some slot names is read
 // once, whatever the number of its slots.  matvec_kernel (below) is the path;
-// matvec_plain_kernel serves rows shorter than one of its steps and rows that
-// do not fit in LDS.
+// matvec_plain_kernel serves rows shorter than one of its steps, rows that do
+// not fit in LDS and experts of 4 GB and more.
 #include "w4a8_launch.h"
 
 #include <hip/hip_runtime.h>
@@ -190,7 +190,6 @@ matvec_kernel(const MatvecArgs a, int rows_max) {
   constexpr bool DIAG = FMT != F_MX;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int n16 = lane & 15, q = lane >> 4;
   const int NP = a.K >> 5;                            // pieces of 32 K
   const int steps = (a.K + MV_STEP - 1) / MV_STEP;
   const int mine = (steps - wave + MV_WAVES - 1) / MV_WAVES;   // this wave's steps of a unit
@@ -245,10 +244,9 @@ matvec_kernel(const MatvecArgs a, int rows_max) {
                              (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(same >> 32), leader) << 32;
     const int M = nu > 0 ? __popcll(members) : 0;
     const float gs = a.gs ? a.gs[e] : 1.0f;
-    const uint8_t* Be = a.B + (size_t)e * a.N * (size_t)(a.K >> 1);
-    const size_t sstride = (size_t)(a.K / GROUP) * (FMT == F_INT ? 2 : 1);   // scale bytes of a column
-    const uint8_t* Se = (const uint8_t*)a.SB + (size_t)e * a.N * sstride;
-    const uint8_t* Ze = FMT == F_INT && a.zeros ? a.zeros + (size_t)e * a.N * (size_t)(a.K / GROUP) : nullptr;
+    const uint8_t* Be = a.B + (uint64_t)(uint32_t)e * a.wexp;
+    const uint8_t* Se = (const uint8_t*)a.SB + (uint64_t)(uint32_t)e * a.sexp;
+    const uint8_t* Ze = FMT == F_INT && a.zeros ? a.zeros + (uint64_t)(uint32_t)e * a.zexp : nullptr;
 
     for (int r0 = 0; r0 < M; r0 += rows_max) {
       const int rows = min(rows_max, M - r0);
@@ -279,61 +277,63 @@ matvec_kernel(const MatvecArgs a, int rows_max) {
       }
       // INT4: each unit's elements in the order 0 4 1 5 2 6 3 7, as
       // int4_to_bf16 has the weights, and the sum of every piece (four lanes)
+      // (XR rows at a time)
       auto x_finish = [&]() __attribute__((always_inline)) {
-        for (int r = 0; r < rows; ++r) {
+        constexpr int XR = 4;
+        for (int r0 = 0; r0 < rows; r0 += XR) {
           for (int v = tid; v < per_x; v += MV_THREADS) {
-            v4u* at = reinterpret_cast<v4u*>(xs + r * pitch + v * 16);
-            const v4u w = *at;
-            float t = 0.f;
+            v4u w[XR];
+            float t[XR];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) t += __uint_as_float(w[i] << 16) + __uint_as_float(w[i] & 0xffff0000u);
-            t += __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(t), 0xB1, 0xf, 0xf, false));  // lane ^ 1
-            t += __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(t), 0x4E, 0xf, 0xf, false));  // lane ^ 2
-            if ((v & 3) == 0) xsum[r * steps * 8 + (v >> 2)] = t;
-            *at = v4u{__builtin_amdgcn_perm(w[2], w[0], 0x05040100u), __builtin_amdgcn_perm(w[2], w[0], 0x07060302u),
-                      __builtin_amdgcn_perm(w[3], w[1], 0x05040100u), __builtin_amdgcn_perm(w[3], w[1], 0x07060302u)};
+            for (int r = 0; r < XR; ++r)
+              w[r] = *reinterpret_cast<const v4u*>(xs + min(r0 + r, rows - 1) * pitch + v * 16);
+#pragma unroll
+            for (int r = 0; r < XR; ++r) {
+              t[r] = 0.f;
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                t[r] += __uint_as_float(w[r][i] << 16) + __uint_as_float(w[r][i] & 0xffff0000u);
+              t[r] += __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(t[r]), 0xB1, 0xf, 0xf, false));  // lane ^ 1
+              t[r] += __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(t[r]), 0x4E, 0xf, 0xf, false));  // lane ^ 2
+            }
+#pragma unroll
+            for (int r = 0; r < XR; ++r) {
+              if (r0 + r >= rows) break;
+              if ((v & 3) == 0) xsum[(r0 + r) * steps * 8 + (v >> 2)] = t[r];
+              *reinterpret_cast<v4u*>(xs + (r0 + r) * pitch + v * 16) =
+                  v4u{__builtin_amdgcn_perm(w[r][2], w[r][0], 0x05040100u), __builtin_amdgcn_perm(w[r][2], w[r][0], 0x07060302u),
+                      __builtin_amdgcn_perm(w[r][3], w[r][1], 0x05040100u), __builtin_amdgcn_perm(w[r][3], w[r][1], 0x07060302u)};
+            }
           }
         }
       };
 
-      // this lane's rows of x in operand order; the zeros stay where they are
-      const uint8_t* xl[TB];
-      bool xlive[TB];
-#pragma unroll
-      for (int tb = 0; tb < TB; ++tb) {
-        const int t = DIAG ? 4 * tb + (n16 >> 2) : min(n16, rows - 1);
-        const bool live = !DIAG || ((n16 & 3) == q && t < rows);
-        xl[tb] = live ? xs + t * pitch + 128 * q : zero;
-        xlive[tb] = live;
-      }
-
       // loads: a wave-uniform base (unit, step) plus the lane's offset
       v4u wa[MV_DEPTH], wb[MV_DEPTH];
       Scales<FMT, GROUP> sc[MV_DEPTH];
-      const size_t wstride = (size_t)(a.K >> 1);
       const uint8_t *ub = nullptr, *us = nullptr, *uz = nullptr;
       uint32_t va = 0, vb = 0, vs = 0, vz = 0;
       auto point = [&](int cb) __attribute__((always_inline)) {
         const int last = a.N - 1 - cb * 16;   // columns past it repeat it
-        ub = Be + (size_t)cb * 16 * wstride;
-        us = Se + (size_t)cb * 16 * sstride;
-        va = (uint32_t)min(lane >> 3, last) * (uint32_t)wstride + (lane & 7) * 16;
-        vb = (uint32_t)min((lane >> 3) + 8, last) * (uint32_t)wstride + (lane & 7) * 16;
-        vs = (uint32_t)min(n16, last) * (uint32_t)sstride + (FMT == F_MX ? 2 * q : 0);
+        ub = Be + (uint32_t)cb * 16u * a.wcol;
+        us = Se + (uint32_t)cb * 16u * a.scol;
+        va = (uint32_t)min(lane >> 3, last) * a.wcol + (lane & 7) * 16;
+        vb = (uint32_t)min((lane >> 3) + 8, last) * a.wcol + (lane & 7) * 16;
+        vs = (uint32_t)min(lane & 15, last) * a.scol + (FMT == F_MX ? 2 * (lane >> 4) : 0);
         if (FMT == F_INT) {   // without zero points the loads read scales, unused
-          uz = Ze ? Ze + (size_t)cb * 16 * (size_t)(a.K / GROUP) : us;
-          vz = (uint32_t)min(n16, last) * (uint32_t)(a.K / GROUP);
+          uz = Ze ? Ze + (uint32_t)cb * 16u * a.zcol : us;
+          vz = (uint32_t)min(lane & 15, last) * a.zcol;
         }
       };
       auto load = [&](int st, int slot) __attribute__((always_inline)) {
         const int p = min(8 * st, NP - 8);   // a wave without steps reads the last one, unused
-        const uint8_t* b = ub + (size_t)p * 16;
+        const uint8_t* b = ub + (uint32_t)p * 16u;
         wa[slot] = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(b + va));
         wb[slot] = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(b + vb));
         constexpr int PG = GROUP >= 32 ? GROUP / 32 : 1;
-        const size_t g = FMT == F_MX ? p : FMT == F_NV ? 2 * p : 2 * (p / PG);
+        const uint32_t g = FMT == F_MX ? p : FMT == F_NV ? 2 * p : 2 * (p / PG);
         __builtin_memcpy(sc[slot].c, us + g + vs, Scales<FMT, GROUP>::BYTES);
-        if (FMT == F_INT) __builtin_memcpy(sc[slot].z, uz + p / PG + vz, Scales<FMT, GROUP>::NG);
+        if (FMT == F_INT) __builtin_memcpy(sc[slot].z, uz + (uint32_t)(p / PG) + vz, Scales<FMT, GROUP>::NG);
       };
 
       v4f acc4 = {0.f, 0.f, 0.f, 0.f};
@@ -347,9 +347,30 @@ matvec_kernel(const MatvecArgs a, int rows_max) {
           if (lcb + 1 < cb0 + nu) point(++lcb);   // past the last unit: its loads once more, never used
         }
       };
+      // the first weights behind x; then this wave's part of x has landed once
+      // no more than those are in flight
+      point(lcb);
+#pragma unroll
+      for (int k = 0; k < MV_DEPTH - 1; ++k) load_next(k);
+      // what the steps need of the lane's place is computed from here on, under
+      // the loads (opaque, or the compiler moves it in front of them)
+      int place = tid;
+      asm volatile("" : "+v"(place));
+      const int ln = place & 63, n16 = ln & 15, q = ln >> 4;
+      // this lane's rows of x in operand order; the zeros stay where they are
+      const uint8_t* xl[TB];
+      bool xlive[TB];
+#pragma unroll
+      for (int tb = 0; tb < TB; ++tb) {
+        const int t = DIAG ? 4 * tb + (n16 >> 2) : min(n16, rows - 1);
+        const bool live = !DIAG || ((n16 & 3) == q && t < rows);
+        xl[tb] = live ? xs + t * pitch + 128 * q : zero;
+        xlive[tb] = live;
+      }
+
       // one step of the product
       auto step = [&](int st, int slot) __attribute__((always_inline)) {
-        const int lc = lane >> 3, lp = lane & 7;
+        const int lc = ln >> 3, lp = ln & 7;
         *reinterpret_cast<v4u*>(wbuf + lc * 128 + ((lp ^ wkey(lc)) << 4)) = wa[slot];
         *reinterpret_cast<v4u*>(wbuf + (lc + 8) * 128 + ((lp ^ wkey(lc + 8)) << 4)) = wb[slot];
         __builtin_amdgcn_wave_barrier();
@@ -452,20 +473,15 @@ matvec_kernel(const MatvecArgs a, int rows_max) {
           }
         }
         lds_barrier();
-        const int t = tid >> 4, n = cb * 16 + (tid & 15);
+        const int t = place >> 4, n = cb * 16 + (place & 15);
         if (t < rows && n < a.N) {
           float v = 0.f;
 #pragma unroll
-          for (int w = 0; w < MV_WAVES; ++w) v += rd[(w * rows_max + t) * 16 + (tid & 15)];
+          for (int w = 0; w < MV_WAVES; ++w) v += rd[(w * rows_max + t) * 16 + (place & 15)];
           a.y[(size_t)slots[t] * a.N + n] = __builtin_bit_cast(uint16_t, (__bf16)(v * gs));
         }
       };
 
-      // the first weights behind x; then this wave's part of x has landed once
-      // no more than those are in flight
-      point(lcb);
-#pragma unroll
-      for (int k = 0; k < MV_DEPTH - 1; ++k) load_next(k);
       wait_loads<3 * (MV_DEPTH - 1)>();
       if constexpr (FMT == F_INT) x_finish();
       lds_barrier();
@@ -536,7 +552,7 @@ hipError_t launch_waves(const MatvecArgs& a, int cus, int64_t units, hipStream_t
 
 hipError_t launch_matvec(const MatvecArgs& a, int cus, hipStream_t stream) {
   const int steps = (a.K + MV_STEP - 1) / MV_STEP;
-  if (a.K < MV_STEP || mv_lds_bytes(8, steps, 1) > MV_LDS) {
+  if (a.K < MV_STEP || mv_lds_bytes(8, steps, 1) > MV_LDS || (int64_t)a.N * (a.K >> 1) >= (int64_t)1 << 32) {
     const dim3 grid((a.N + 3) / 4, a.S), block(256);
     if (a.fmt == F_MX) hipLaunchKernelGGL(matvec_plain_kernel<F_MX>, grid, block, 0, stream, a);
     else if (a.fmt == F_NV) hipLaunchKernelGGL(matvec_plain_kernel<F_NV>, grid, block, 0, stream, a);

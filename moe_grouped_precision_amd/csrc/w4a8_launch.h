@@ -73,6 +73,8 @@ struct MatvecArgs {
   uint16_t* y;             // [S][N] bf16
   int S, E, N, K, fmt, group;
   int per_row_inv;         // slot s multiplies row (s * per_row_inv) >> 16 of x (s < 64)
+  // bytes of a column and of an expert (the path needs an expert's weights below 2^32 bytes)
+  uint32_t wcol, scol, zcol, wexp, sexp, zexp;
 };
 hipError_t launch_matvec(const MatvecArgs& args, int cus, hipStream_t stream);
 hipError_t launch_swiglu(const uint16_t* C, int R, int I, uint16_t* h, uint8_t* codes, float* scales,

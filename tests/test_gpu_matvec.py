@@ -95,6 +95,15 @@ def test_experts(gpu_lib, fmt, group, T, k, per_slot, E, N, K):
         assert not y[2].any() and not y[T * k - 1].any()
 
 
+@pytest.mark.parametrize("fmt,group", [(MX, 32), (NV, 16), (INT4, 128)])
+@pytest.mark.parametrize("X,K", [(2, 32768), (1, 66048), (2, 131072), (3, 224)])
+def test_long_and_short_rows(gpu_lib, fmt, group, X, K):
+    """Rows of x that fill the LDS, that do not fit in it, and shorter than a step."""
+    K = K // max(32, group) * max(32, group)
+    x, B, SB, z, s = _problem(fmt, X, 1, 19, K, group, K % 1000)
+    _check(gpu_lib, fmt, x, B, SB, z, s, None, f"dense fmt={fmt} group={group} X={X} N=19 K={K}")
+
+
 def test_repeats_streams_and_expert_scale_default(gpu_lib):
     x, B, SB, z, _ = _problem(INT4, 4, 3, 50, 512, 64, 5)
     ids = torch.tensor([0, 2, 2, 1], dtype=torch.int32)
