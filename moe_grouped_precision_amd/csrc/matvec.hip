@@ -11,6 +11,7 @@
 // once, whatever the number of its slots.  matvec_kernel (below) is the path;
 // matvec_plain_kernel serves rows shorter than one of its steps, rows that do
 // not fit in LDS and experts of 4 GB and more.
+#include "w4a8_device.h"
 #include "w4a8_launch.h"
 
 #include <hip/hip_runtime.h>
@@ -176,12 +177,6 @@ __device__ __forceinline__ void load_to_lds(const void* src, uint8_t* to) {
 template <int N>
 __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
 
-// position of the i-th set bit of m (i below its number of set bits)
-__device__ __forceinline__ int nth_bit(uint64_t m, int i) {
-  for (; i > 0; --i) m &= m - 1;
-  return __ffsll((unsigned long long)m) - 1;
-}
-
 // TB: sets of four tokens (MXFP4: one set of sixteen, TB = 1).
 template <int FMT, int GROUP, int TB, int MV_WAVES>
 __global__ void __launch_bounds__(64 * MV_WAVES, mv_per_cu(MV_WAVES, TB) * MV_WAVES / 4)
@@ -216,8 +211,12 @@ matvec_kernel(const MatvecArgs a, int rows_max) {
     const uint64_t set = __ballot(id & bit);
     same &= (id & bit) ? set : ~set;
   }
-  const uint64_t leaders = __ballot(id >= 0 && (same & ((1ull << lane) - 1)) == 0);
-  const int D = __popcll(leaders);
+  // an item: up to rows_max slots of one expert; a leader lane (an expert's
+  // first slot) holds its expert's items before[..] .. upto[..]
+  const bool first = id >= 0 && (same & ((1ull << lane) - 1)) == 0;
+  const int mine_items = first ? (__popcll(same) + rows_max - 1) / rows_max : 0;
+  const int upto = wave_inclusive_sum(mine_items), before = upto - mine_items;
+  const int D = __builtin_amdgcn_readlane(upto, 63);
   const int UB = (a.N + 15) >> 4;                     // units of an expert
 
   // slots without an expert: zeros
@@ -230,27 +229,26 @@ matvec_kernel(const MatvecArgs a, int rows_max) {
   uint32_t nib = 0x00780078u, one16 = 0x41804180u;
   asm volatile("" : "+s"(nib), "+v"(one16));
   int parity = 0;
-  // every expert has an equal number of workgroups, a workgroup one expert and
-  // a run of its units
+  // every item has an equal number of workgroups, a workgroup one item and a
+  // run of its units
   const uint32_t each = D ? gridDim.x / (uint32_t)D : 1u;
   const uint32_t d = blockIdx.x / each, w0 = blockIdx.x - d * each;
   if (d < (uint32_t)D) {
     const uint32_t share = UB / each, more = UB % each;
     const int cb0 = share * w0 + min(w0, more);
     const int nu = share + (w0 < more ? 1u : 0u);
-    const int leader = nth_bit(leaders, d);
+    const int leader = __ffsll((unsigned long long)__ballot(before <= (int)d && (int)d < upto)) - 1;
     const int e = __builtin_amdgcn_readlane(id, leader);
     const uint64_t members = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)same, leader) |
                              (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(same >> 32), leader) << 32;
-    const int M = nu > 0 ? __popcll(members) : 0;
+    const int r0 = ((int)d - __builtin_amdgcn_readlane(before, leader)) * rows_max;
+    const int rows = min(rows_max, (int)__popcll(members) - r0);
     const float gs = a.gs ? a.gs[e] : 1.0f;
     const uint8_t* Be = a.B + (uint64_t)(uint32_t)e * a.wexp;
     const uint8_t* Se = (const uint8_t*)a.SB + (uint64_t)(uint32_t)e * a.sexp;
     const uint8_t* Ze = FMT == F_INT && a.zeros ? a.zeros + (uint64_t)(uint32_t)e * a.zexp : nullptr;
 
-    for (int r0 = 0; r0 < M; r0 += rows_max) {
-      const int rows = min(rows_max, M - r0);
-      lds_barrier();   // the previous pass's x and slots are no longer read
+    if (nu > 0) {
       {  // every wave writes the same list
         const int rank = __popcll(members & ((1ull << lane) - 1)) - r0;
         if (((members >> lane) & 1) && rank >= 0 && rank < rows) slots[rank] = lane;
@@ -530,16 +528,18 @@ hipError_t launch_sets(const MatvecArgs& a, int rows, int grid, int lds, hipStre
 
 template <int WAVES>
 hipError_t launch_waves(const MatvecArgs& a, int cus, int64_t units, hipStream_t stream) {
-  // rows of a pass: all of a dense call's, twice the mean of an expert's (at
+  // rows of an item: all of a dense call's, twice the mean of an expert's (at
   // least four), as far as the LDS holds them; then as many workgroups per CU
-  // as there are units, registers and LDS for
+  // as there are units, registers and LDS for (and one per slot at least: an
+  // item has a slot)
   const int steps = (a.K + MV_STEP - 1) / MV_STEP;
   int rows = std::min(std::min(a.S, 16), a.ids ? std::max(4, 2 * ((a.S + a.E - 1) / a.E)) : 16);
   int per_cu = (int)std::min<int64_t>(mv_per_cu(WAVES, a.fmt != F_MX && rows > 8 ? 4 : 1),
                                       std::max<int64_t>(1, (units + cus - 1) / cus));
   while (per_cu > 1 && mv_lds_bytes(WAVES, steps, std::min(rows, 4)) > MV_LDS / per_cu) --per_cu;
   while (rows > 1 && mv_lds_bytes(WAVES, steps, rows) > MV_LDS / per_cu) --rows;
-  const int grid = (int)std::min<int64_t>(units, (int64_t)per_cu * cus);
+  const int64_t work = units * (a.ids ? 1 : (a.S + rows - 1) / rows);
+  const int grid = std::max(a.S, (int)std::min<int64_t>(work, (int64_t)per_cu * cus));
   const int lds = mv_lds_bytes(WAVES, steps, rows);
   if (a.fmt == F_MX) return launch_sets<F_MX, 32, WAVES>(a, rows, grid, lds, stream);
   if (a.fmt == F_NV) return launch_sets<F_NV, 16, WAVES>(a, rows, grid, lds, stream);
