@@ -17,7 +17,13 @@
 // its halves, k rounds of a wave maximum.  Wider rows take one workgroup, up
 // to 1024 experts per wave, 16 in a lane's registers; there the k-th largest
 // of 64 group maxima bounds the selection from below, the few experts that
-// reach it are collected in LDS and ranked by counting.
+// reach it are collected in LDS and ranked by counting.  (Ranking by k rounds
+// of a maximum over all of a lane's experts took 53 us on 2047 x 6144.)
+//
+// What it measured in the kernel: 64 x 32 3.0 us and the gradient of 16384 x
+// 32 4.7 us, both at the length of a launch and one trip to memory; 2047 x
+// 6144 bf16 9.4 to 10.8 us (25 MB: 2.5 TB/s), bound by the three barriers of
+// a row and the rounds of a maximum between them, with 8 rows on a CU.
 #include "swiglu.h"
 #include "w4a8_launch.h"
 

@@ -84,9 +84,19 @@ matvec_plain_kernel(const MatvecArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// The path.  A workgroup of four waves takes a run of units (expert, 16
-// columns); its waves share a unit's K in steps of 256 (wave w takes steps w,
-// w + 4, ...) and join their sums in LDS.
+// The path.  A workgroup takes one item (up to rows_max slots of one expert)
+// and a run of its units (16 columns); its four or eight waves share a unit's
+// K in steps of 256 (wave w takes steps w, w + waves, ...) and join their
+// sums in LDS.
+//
+// What it measured (weights not in the caches): 8 experts 4096 x 6144, one
+// token, MXFP4 19.7 us (107 MB: 5.4 TB/s), NVFP4 21.0, INT4 per 128 22.3; 64
+// slots of 32 such experts 65 us (386 MB: 5.9 TB/s); 65536 x 6144 dense 36.5
+// us (214 MB: 5.9 TB/s).  Bound by HBM, after 3 to 4 us of start (ids, x and
+// the first weights, each a trip to memory, and code read for the first time
+// in the launch).  Four steps in registers instead of three: 2% more on the
+// long shapes, 10% less on one row of 6144 x 6144 (more code); four
+// workgroups per CU instead of three: 29.2 against 26.8 us on 131072 x 2048.
 //
 // Weights: per step a wave reads 16 columns x 128 bytes as two loads of eight
 // whole 128-byte lines (lane l: column l / 8, 16-byte piece l % 8, one piece
@@ -512,9 +522,11 @@ constexpr int MV_LDS = 160 * 1024;   // of a CU
 
 template <int FMT, int GROUP, int TB, int WAVES>
 hipError_t launch_path(const MatvecArgs& a, int rows, int grid, int lds, hipStream_t stream) {
-  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&matvec_kernel<FMT, GROUP, TB, WAVES>),
-                                           hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-  if (e != hipSuccess) return e;
+  if (lds > 64 * 1024) {   // past what a launch may have without asking
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&matvec_kernel<FMT, GROUP, TB, WAVES>),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    if (e != hipSuccess) return e;
+  }
   hipLaunchKernelGGL((matvec_kernel<FMT, GROUP, TB, WAVES>), dim3(grid), dim3(64 * WAVES), lds, stream, a, rows);
   return hipGetLastError();
 }
@@ -560,11 +572,11 @@ hipError_t launch_matvec(const MatvecArgs& a, int cus, hipStream_t stream) {
     return hipGetLastError();
   }
   // Eight waves where a CU gets one workgroup in any case: not enough units
-  // for two (INT4, 5 rows of 6144 x 3583: 12.0 against 13.3 us with four), or
-  // so many rows of x that the LDS holds no second (16 rows of 6144 x 6144,
-  // MXFP4: 16.8 against 23.9 us, NVFP4: 22.9 against 26.5).  Else four (one
-  // token of 8 experts 4096 x 6144, INT4: 21.7 against 22.5 us; 24 slots of
-  // 6144 x 2048, NVFP4: 25.8 against 27.4).
+  // for two (one row of 2048 x 6144, MXFP4: 8.6 against 10.3 us with four, 5
+  // rows of 3583 x 6144, INT4: 10.8 against 11.2), or so many rows of x that
+  // the LDS holds no second (16 rows of 6144 x 6144: MXFP4 12.4 against 14.0
+  // us, INT4 22.5 against 23.8, NVFP4 17.6 against 17.3).  Else four (24 slots
+  // of 6144 x 2048: NVFP4 25.8 against 27.4 us, INT4 28.0 against 32.9).
   const int64_t units = (int64_t)std::min(a.S, a.E) * ((a.N + 15) / 16);
   if (units <= cus || (!a.ids && a.S > 8)) return launch_waves<8>(a, cus, units, stream);
   return launch_waves<4>(a, cus, units, stream);
