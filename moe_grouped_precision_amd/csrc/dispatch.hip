@@ -129,10 +129,11 @@ dispatch_backward_kernel(const uint16_t* __restrict__ dA, int R, int K, const in
   }
 }
 
-// Two waves per slot, each with six chunks of C and of dout in flight (dout's
-// row is shared by the token's slots through the caches): 1152 x 6144, top-8
-// 45.4 us, 5.3 TB/s; one wave and one chunk 53.0, one wave and six 46.1, four
-// waves and three 49.0.
+// Two waves per slot, each with six chunks of C and of dout in flight: 1152 x
+// 6144, top-8 45.3 us; one wave and one chunk 53.0, one wave and six 46.1,
+// four waves and three 49.0.  Workgroups go to the 8 XCDs in turn, so four
+// neighbouring ones (8 slots: mostly one token's) are dealt to the same XCD, whose
+// L2 then serves dout's row to all of them (44.7 us, 5.3 TB/s).
 constexpr int C_SPLIT = 2, C_CHUNKS = 6, C_WAVES = 4;
 template <int W>
 __global__ void __launch_bounds__(64 * C_WAVES)
@@ -141,7 +142,8 @@ combine_backward_kernel(const uint16_t* __restrict__ C, const uint16_t* __restri
                         int top_k, uint16_t* __restrict__ dC, float* __restrict__ dweights) {
   __shared__ float part[C_WAVES];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t s = (int64_t)blockIdx.x * (C_WAVES / C_SPLIT) + wave / C_SPLIT;
+  const uint32_t b = (blockIdx.x & ~31u) | (blockIdx.x & 7u) << 2 | (blockIdx.x >> 3 & 3u);
+  const int64_t s = (int64_t)b * (C_WAVES / C_SPLIT) + wave / C_SPLIT;
   const int r = s < slots ? row_of_slot[s] : -1;
   float dot = 0.f;
   if (r >= 0 && r < R) {
@@ -221,7 +223,7 @@ hipError_t launch_combine_backward(const uint16_t* C, const uint16_t* dout, int 
                                    hipStream_t stream) {
   const int64_t slots = (int64_t)T * top_k;
   constexpr int per_wg = C_WAVES / C_SPLIT;
-  const dim3 grid((unsigned)((slots + per_wg - 1) / per_wg)), block(64 * C_WAVES);
+  const dim3 grid((unsigned)((slots + per_wg * 32 - 1) / (per_wg * 32) * 32)), block(64 * C_WAVES);   // see b
   if (wide(N, C, dout, dC))
     hipLaunchKernelGGL(combine_backward_kernel<8>, grid, block, 0, stream, C, dout, R, N, row_of_slot, weights, slots,
                        top_k, dC, dweights);
