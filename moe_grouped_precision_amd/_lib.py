@@ -19,6 +19,9 @@ _STATUS = {0: "W4A8_OK", 1: "W4A8_ERR_NULL", 2: "W4A8_ERR_SHAPE", 3: "W4A8_ERR_L
 
 _lib = None
 _ready = set()  # devices that were found to be gfx950
+_Tensor, _bfloat16 = torch.Tensor, torch.bfloat16
+# without torch.cuda's checks around it: asked only once a device is in _ready
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 class W4A8Error(RuntimeError):
@@ -93,7 +96,7 @@ def load(require_device: bool = True):
         lib = ctypes.CDLL(_LIB_PATH)
         _declare(lib)
         _lib = lib
-    if require_device and not (_ready and torch.cuda.current_device() in _ready):
+    if require_device and not (_ready and _current_device() in _ready):
         if not torch.cuda.is_available():
             raise RuntimeError("libw4a8 needs a visible MI355X (gfx950) GPU")
         dev = torch.cuda.current_device()
@@ -121,10 +124,13 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 def _stream():
     if _raw_stream is None:
         return torch.cuda.current_stream().cuda_stream
-    return _raw_stream(torch.cuda.current_device())
+    return _raw_stream(_current_device())
 
 
 def _need(t: torch.Tensor, name: str, dtype, numel: Optional[int] = None):
+    if isinstance(t, _Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous() and (
+            numel is None or t.numel() == numel):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if not t.is_cuda:
@@ -447,9 +453,10 @@ def _logits_type(t: torch.Tensor) -> int:
 
 
 def _bf16(t: torch.Tensor, name: str, numel: Optional[int] = None):
-    if isinstance(t, torch.Tensor) and t.dtype not in (torch.bfloat16, torch.uint16, torch.int16):
+    dtype = getattr(t, "dtype", None)
+    if dtype is not _bfloat16 and isinstance(t, _Tensor) and dtype not in (torch.uint16, torch.int16):
         raise TypeError(f"{name} must be bfloat16 (or 16-bit integer bits)")
-    _need(t, name, getattr(t, "dtype", None), numel)
+    _need(t, name, dtype, numel)
 
 
 def topk_gate(logits: torch.Tensor, top_k: int, score: int = GATE_SOFTMAX, renorm: bool = True, scale: float = 1.0,

@@ -14,10 +14,10 @@
 //   sigmoid, renorm  dl_i = u_i (g_i - sum_j g_j u_j) (1 - s_i)
 //
 // Rows of up to 64 experts: one expert per lane, one row per wave or two in
-// its halves, k rounds of a wave maximum.  Wider rows take one workgroup, up
-// to 1024 experts per wave, 16 in a lane's registers; there the k-th largest
-// of 64 group maxima bounds the selection from below, the few experts that
-// reach it are collected in LDS and ranked by counting.  (Ranking by k rounds
+// its halves, k rounds of a wave maximum.  Wider rows take one workgroup, 4 to
+// 24 experts in a lane's registers (up to 1536 per wave); there the k-th
+// largest of 64 group maxima bounds the selection from below, the few experts
+// that reach it are collected in LDS and ranked by counting.  (Ranking by k rounds
 // of a maximum over all of a lane's experts took 53 us on 2047 x 6144.)
 //
 // What it measured in the kernel: 64 x 32 3.0 us and the gradient of 16384 x
