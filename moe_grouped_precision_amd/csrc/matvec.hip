@@ -90,13 +90,15 @@ matvec_plain_kernel(const MatvecArgs a) {
 // sums in LDS.
 //
 // What it measured (weights not in the caches): 8 experts 4096 x 6144, one
-// token, MXFP4 19.7 us (107 MB: 5.4 TB/s), NVFP4 21.0, INT4 per 128 22.3; 64
-// slots of 32 such experts 65 us (386 MB: 5.9 TB/s); 65536 x 6144 dense 36.5
-// us (214 MB: 5.9 TB/s).  Bound by HBM, after 3 to 4 us of start (ids, x and
+// token, MXFP4 19.4 us (107 MB: 5.5 TB/s), NVFP4 20.7, INT4 per 128 22.3; 64
+// slots of 32 such experts 65 us (386 MB: 5.9 TB/s); 65536 x 6144 dense 35.8
+// us (214 MB: 6.0 TB/s).  Bound by HBM, after 3 to 4 us of start (ids, x and
 // the first weights, each a trip to memory, and code read for the first time
 // in the launch).  Four steps in registers instead of three: 2% more on the
 // long shapes, 10% less on one row of 6144 x 6144 (more code); four
-// workgroups per CU instead of three: 29.2 against 26.8 us on 131072 x 2048.
+// workgroups per CU instead of three: 29.2 against 26.8 us on 131072 x 2048.  The loads that run past the last
+// unit read one place only: 9 of 12 surplus MB less in 131 MB of NVFP4, 26.5 to
+// 25.2 us.
 //
 // Weights: per step a wave reads 16 columns x 128 bytes as two loads of eight
 // whole 128-byte lines (lane l: column l / 8, 16-byte piece l % 8, one piece
@@ -333,8 +335,16 @@ matvec_kernel(const MatvecArgs a, int rows_max) {
           vz = (uint32_t)min(lane & 15, last) * a.zcol;
         }
       };
+      // loads past the last unit, or of a wave without steps, are never used:
+      // every lane reads one place
+      auto aside = [&]() __attribute__((always_inline)) {
+        va = 0;
+        vb = 0;
+        vs = 0;
+        if (FMT == F_INT) vz = 0;
+      };
       auto load = [&](int st, int slot) __attribute__((always_inline)) {
-        const int p = min(8 * st, NP - 8);   // a wave without steps reads the last one, unused
+        const int p = min(8 * st, NP - 8); 
         const uint8_t* b = ub + (uint32_t)p * 16u;
         wa[slot] = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(b + va));
         wb[slot] = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(b + vb));
@@ -352,12 +362,16 @@ matvec_kernel(const MatvecArgs a, int rows_max) {
         load(wave + MV_WAVES * li, slot);
         if (++li == mine) {
           li = 0;
-          if (lcb + 1 < cb0 + nu) point(++lcb);   // past the last unit: its loads once more, never used
+          if (lcb + 1 < cb0 + nu)
+            point(++lcb);
+          else
+            aside();
         }
       };
       // the first weights behind x; then this wave's part of x has landed once
       // no more than those are in flight
       point(lcb);
+      if (mine <= 0) aside();
 #pragma unroll
       for (int k = 0; k < MV_DEPTH - 1; ++k) load_next(k);
       // what the steps need of the lane's place is computed from here on, under
