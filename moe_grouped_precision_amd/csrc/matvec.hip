@@ -96,9 +96,9 @@ matvec_plain_kernel(const MatvecArgs a) {
 // the first weights, each a trip to memory, and code read for the first time
 // in the launch).  Four steps in registers instead of three: 2% more on the
 // long shapes, 10% less on one row of 6144 x 6144 (more code); four
-// workgroups per CU instead of three: 29.2 against 26.8 us on 131072 x 2048.  The loads that run past the last
-// unit read one place only: 9 of 12 surplus MB less in 131 MB of NVFP4, 26.5 to
-// 25.2 us.
+// workgroups per CU instead of three: 29.2 against 26.8 us on 131072 x 2048.
+// Letting the loads past a workgroup's last unit read that unit again: 26.5
+// against 25.2 us on 24 NVFP4 slots of 6144 x 2048 (154 against 143 MB read).
 //
 // Weights: per step a wave reads 16 columns x 128 bytes as two loads of eight
 // whole 128-byte lines (lane l: column l / 8, 16-byte piece l % 8, one piece
