@@ -515,8 +515,7 @@ matvec_kernel(const MatvecArgs a, int rows_max) {
         for (int t = 0; t < total; t += MV_DEPTH) {
 #pragma unroll
           for (int k = 0; k < MV_DEPTH; ++k) {
-            // loads in every turn, so that each wait is one constant: past the
-            // end they read the last unit again
+            // loads in every turn, so that each wait is one constant
             load_next((k + MV_DEPTH - 1) % MV_DEPTH);
             if (t + k < total) {
               step(wave + MV_WAVES * si, k);
