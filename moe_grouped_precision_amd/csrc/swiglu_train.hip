@@ -137,12 +137,15 @@ swiglu_backward_kernel(const uint8_t* __restrict__ codes, const float* __restric
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     // g = code * q needs 28 bits: what fp32 cuts off it (lo) would cost |g|
-    // times its size in e^-g, so e^-(g + lo) = e^-g (1 - lo).  e^-g is capped
-    // at e^88, where it and its reciprocal stay finite.
+    // times its size in e^-g, so e^-(g + lo) = e^-g (1 - lo) where |g| < 104
+    // (there |lo| <= 2^-18; for larger gates lo reaches 1 and more, and s is
+    // 0 or 1 without it).  e^-g is capped at e^88, where it and its reciprocal
+    // stay finite; from -104 down s is below half of fp32's smallest value and
+    // taken as 0, or g s would grow with |g|.
     const float gv = fg[e] * qg, lo = fmaf(fg[e], qg, -gv), uv = fu[e] * qu;
     const float x0 = exp_f32(fminf(-gv, 88.0f));
-    const float x = fmaf(-x0, lo, x0);
-    const float s = __builtin_amdgcn_rcpf(1.0f + x);
+    const float x = fabsf(gv) < 104.0f ? fmaf(-x0, lo, x0) : x0;
+    const float s = gv <= -104.0f ? 0.0f : __builtin_amdgcn_rcpf(1.0f + x);
     const float silu = gv * s;
     dg[e] = fd[e] * uv * (s * fmaf(gv, x * s, 1.0f));
     du[e] = fd[e] * silu;
