@@ -146,8 +146,11 @@ swiglu_backward_kernel(const uint8_t* __restrict__ codes, const float* __restric
     const float x0 = exp_f32(fminf(-gv, 88.0f));
     const float x = fabsf(gv) < 104.0f ? fmaf(-x0, lo, x0) : x0;
     const float s = gv <= -104.0f ? 0.0f : __builtin_amdgcn_rcpf(1.0f + x);
-    const float silu = gv * s;
-    dg[e] = fd[e] * uv * (s * fmaf(gv, x * s, 1.0f));
+    const float silu = gv * s, slope = s * fmaf(gv, x * s, 1.0f);
+    // dh u first (u slope may underflow under a large dh); where that leaves
+    // fp32, slope (at most 1.1) goes in between
+    const float du_dh = fd[e] * uv;
+    dg[e] = fabsf(du_dh) < __builtin_inff() ? du_dh * slope : fd[e] * (uv * slope);
     du[e] = fd[e] * silu;
     hh[e] = silu * uv;
   }

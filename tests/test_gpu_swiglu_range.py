@@ -85,3 +85,14 @@ def test_known_gates_of_the_rounding_correction(gpu_lib):
         h = torch.empty_like(dh).cuda()
         dC, h = gpu_lib.swiglu_backward(codes.cuda(), scales.cuda(), dh.cuda(), h=h)
         assert not dC.any() and not h.any()
+
+
+def test_products_that_leave_fp32_in_between(gpu_lib):
+    """dh u is past fp32's largest value, dh u s (1 + g (1 - s)) is not."""
+    rng = np.random.default_rng(5)
+    C = np.empty((6, 2 * I))
+    C[:, :I] = rng.uniform(-80, -60, (6, I))
+    C[:, I:] = rng.uniform(-1, 1, (6, I)) * 2.0 ** 100
+    dh = rng.uniform(-1, 1, (6, I)) * 2.0 ** 70
+    _check(gpu_lib, torch.from_numpy(C.astype(np.float32)).to(torch.bfloat16),
+           torch.from_numpy(dh.astype(np.float32)).to(torch.bfloat16))
