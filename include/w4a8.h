@@ -506,8 +506,12 @@ int w4a8_combine_backward(const uint16_t* C_bf16_dev, const uint16_t* dout_bf16_
  * expert_ids_dev     int32 [S] (w4a8_topk_gate's ids), or NULL with E == 1;
  *                    a slot whose id is outside [0, E) gets zeros.
  * y_bf16_dev         out bf16 [S][N].  4-byte aligned.
- * Sums and scales are fp32, with one rounding to bf16.  NaN scale codes make
- * their columns NaN for the expert's slots.
+ * Sums and scales are fp32, with one rounding to bf16.  An output that does
+ * not come out finite so (scales of 2^126 and 2^127, values of x near the
+ * largest) is computed again in 64 bits: it is finite wherever the formula's
+ * value is, and infinities and NaN in x, weights and scales give the
+ * formula's infinities and NaN.  NaN scale codes make their columns NaN for
+ * the expert's slots.
  * Limits: 0 <= S <= W4A8_MAX_MATVEC_SLOTS, S % X == 0, 1 <= E <=
  * W4A8_MAX_PREP_EXPERTS, 1 <= N <= W4A8_MAX_N, K a multiple of group and of
  * 32, 32 <= K <= W4A8_MAX_K.  S == 0 does nothing.

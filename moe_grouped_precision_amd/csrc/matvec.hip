@@ -49,6 +49,41 @@ __device__ __forceinline__ float group_scale(const void* p, size_t i) {
   return __uint_as_float((uint32_t)((const uint16_t*)p)[i] << 16);
 }
 
+// One output by the definition in 64 bits, in every lane of the wave: for
+// sums that fp32 does not hold on the way (MXFP4 scales of 2^126 and 2^127,
+// whose weights are past bf16 and fp32; sums of x q before a small scale;
+// INT4's 16 + q) or in which an infinity met a weight's offset.  col = e N + n.
+template <int FMT>
+__device__ __forceinline__ float exact_output(const MatvecArgs& a, size_t col, const uint16_t* xr, float gs) {
+  const int lane = threadIdx.x & 63;
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(a.B + col * (size_t)(a.K >> 1));
+  double acc = 0.0;
+  for (int c = lane; c < a.K / 8; c += 64) {
+    const size_t gi = col * (size_t)(a.K / a.group) + (8 * c) / a.group;
+    double sc;
+    if (FMT == F_MX) {
+      const uint32_t code = ((const uint8_t*)a.SB)[gi];
+      sc = code == 0xff ? __builtin_nan("") : __builtin_bit_cast(double, (uint64_t)(code + 896) << 52);
+    } else {
+      sc = group_scale<FMT>(a.SB, gi);
+    }
+    const float z = FMT != F_INT ? 0.f : a.zeros ? (float)a.zeros[gi] : 8.f;
+    const uint32_t v = w[c];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t q = (v >> (4 * i)) & 15u;
+      const double x = __uint_as_float((uint32_t)xr[8 * c + i] << 16);
+      acc += x * ((FMT == F_INT ? (float)q - z : e2m1(q)) * sc);
+    }
+  }
+#pragma unroll
+  for (int i = 1; i < 64; i <<= 1) acc += __shfl_xor(acc, i, 64);
+  return (float)(acc * gs);
+}
+
+// exponent all ones: infinite or NaN
+__device__ __forceinline__ bool not_finite(uint16_t bf16) { return (bf16 & 0x7f80u) == 0x7f80u; }
+
 // One wave per (slot, column).
 template <int FMT>
 __global__ void __launch_bounds__(256)
@@ -58,8 +93,9 @@ matvec_plain_kernel(const MatvecArgs a) {
   const int s = blockIdx.y;
   if (n >= a.N) return;
   const int e = a.ids ? a.ids[s] : 0;
-  float acc = 0.f;
+  uint16_t out = 0;
   if (e >= 0 && e < a.E) {
+    float acc = 0.f;
     const size_t col = (size_t)e * a.N + n;
     const uint16_t* xr = a.x + (size_t)((s * a.per_row_inv) >> 16) * a.K;
     const uint32_t* w = reinterpret_cast<const uint32_t*>(a.B + col * (size_t)(a.K >> 1));
@@ -78,9 +114,11 @@ matvec_plain_kernel(const MatvecArgs a) {
     }
 #pragma unroll
     for (int i = 1; i < 64; i <<= 1) acc += __shfl_xor(acc, i, 64);
-    if (a.gs) acc *= a.gs[e];
+    const float gs = a.gs ? a.gs[e] : 1.0f;
+    out = __builtin_bit_cast(uint16_t, (__bf16)(acc * gs));
+    if (not_finite(out)) out = __builtin_bit_cast(uint16_t, (__bf16)exact_output<FMT>(a, col, xr, gs));
   }
-  if (lane == 0) a.y[(size_t)s * a.N + n] = __builtin_bit_cast(uint16_t, (__bf16)acc);
+  if (lane == 0) a.y[(size_t)s * a.N + n] = out;
 }
 
 // ---------------------------------------------------------------------------
@@ -117,6 +155,12 @@ matvec_plain_kernel(const MatvecArgs a) {
 // (token, lane group), and the scales (and the zero points, as (16 + z) times
 // the sum of x over the piece) are applied to it in fp32.  Four tokens per
 // instruction; MXFP4 takes sixteen.
+//
+// What fp32 or bf16 do not hold on that way shows as an output that is not
+// finite (infinity and NaN never leave a sum again): MXFP4 weights of 2^128
+// and more, sums of x q ahead of a small scale, an infinity in x times 16 + q
+// less the same times 16 + z.  A wave notes such outputs and computes them
+// once more at the end, by exact_output.
 //
 // x (the rows of the unit's expert) is in LDS as bf16, zeros past K.  Where K
 // is no multiple of 256 the last step starts at K - 256: what it repeats
@@ -356,6 +400,7 @@ matvec_kernel(const MatvecArgs a, int rows_max) {
 
       v4f acc4 = {0.f, 0.f, 0.f, 0.f};
       float acc[TB] = {};
+      uint64_t again = 0;             // lanes that wrote an output that is not finite
       const int total = nu * mine;
       int lcb = cb0, li = 0;          // next load
       auto load_next = [&](int slot) __attribute__((always_inline)) {
@@ -496,12 +541,15 @@ matvec_kernel(const MatvecArgs a, int rows_max) {
         }
         lds_barrier();
         const int t = place >> 4, n = cb * 16 + (place & 15);
+        uint16_t out = 0;
         if (t < rows && n < a.N) {
           float v = 0.f;
 #pragma unroll
           for (int w = 0; w < MV_WAVES; ++w) v += rd[(w * rows_max + t) * 16 + (place & 15)];
-          a.y[(size_t)slots[t] * a.N + n] = __builtin_bit_cast(uint16_t, (__bf16)(v * gs));
+          out = __builtin_bit_cast(uint16_t, (__bf16)(v * gs));
+          a.y[(size_t)slots[t] * a.N + n] = out;
         }
+        again |= __ballot(not_finite(out));
       };
 
       wait_loads<3 * (MV_DEPTH - 1)>();
@@ -524,6 +572,34 @@ matvec_kernel(const MatvecArgs a, int rows_max) {
                 finish(cb++);
               }
             }
+          }
+        }
+      }
+
+      // outputs that are not finite once more, each by the whole wave (a lane
+      // reads back what it wrote itself); a row of x with a NaN has its NaN
+      // already.  8 slots of 8 experts 4096 x 6144 with an infinity in x: 0.5 ms.
+      if (__builtin_expect(again != 0, 0)) {
+        uint32_t nan_rows = 0;
+        for (int r = 0; r < rows; ++r) {
+          const uint16_t* xr = a.x + (size_t)((slots[r] * a.per_row_inv) >> 16) * a.K;
+          bool nan = false;
+          for (int c = ln; c < a.K / 2; c += 64) {
+            const uint32_t v = reinterpret_cast<const uint32_t*>(xr)[c];
+            nan |= (v & 0x7fffu) > 0x7f80u || (v & 0x7fff0000u) > 0x7f800000u;
+          }
+          nan_rows |= (__ballot(nan) ? 1u : 0u) << r;
+        }
+        for (int c = cb0; c < cb0 + nu; ++c) {
+          const int t = place >> 4, n = c * 16 + (place & 15);
+          const bool live = t < rows && n < a.N && !((nan_rows >> (t & 31)) & 1u);
+          uint64_t todo = __ballot(live && not_finite(a.y[(size_t)slots[t] * a.N + n]));
+          for (; todo; todo &= todo - 1) {
+            const int b = __ffsll((unsigned long long)todo) - 1;
+            const int slot = __builtin_amdgcn_readfirstlane(slots[(wave * 64 + b) >> 4]), col = c * 16 + (b & 15);
+            const uint16_t* xr = a.x + (size_t)((slot * a.per_row_inv) >> 16) * a.K;
+            const float v = exact_output<FMT>(a, (size_t)e * a.N + col, xr, gs);
+            if (ln == b) a.y[(size_t)slot * a.N + col] = __builtin_bit_cast(uint16_t, (__bf16)v);
           }
         }
       }
