@@ -138,12 +138,12 @@ constexpr int C_SPLIT = 2, C_CHUNKS = 6, C_WAVES = 4;
 template <int W>
 __global__ void __launch_bounds__(64 * C_WAVES)
 combine_backward_kernel(const uint16_t* __restrict__ C, const uint16_t* __restrict__ dout, int R, int N,
-                        const int32_t* __restrict__ row_of_slot, const float* __restrict__ weights, int64_t slots,
-                        int top_k, uint16_t* __restrict__ dC, float* __restrict__ dweights) {
+                        const int32_t* __restrict__ row_of_slot, const float* __restrict__ weights, int64_t first,
+                        int64_t slots, int top_k, uint16_t* __restrict__ dC, float* __restrict__ dweights) {
   __shared__ float part[C_WAVES];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const uint32_t b = (blockIdx.x & ~31u) | (blockIdx.x & 7u) << 2 | (blockIdx.x >> 3 & 3u);
-  const int64_t s = (int64_t)b * (C_WAVES / C_SPLIT) + wave / C_SPLIT;
+  const int64_t s = first + (int64_t)b * (C_WAVES / C_SPLIT) + wave / C_SPLIT;
   const int r = s < slots ? row_of_slot[s] : -1;
   float dot = 0.f;
   if (r >= 0 && r < R) {
@@ -187,10 +187,7 @@ combine_backward_kernel(const uint16_t* __restrict__ C, const uint16_t* __restri
 bool wide(int K, const void* a, const void* b, const void* c = nullptr) {
   return K % 8 == 0 && (((uintptr_t)a | (uintptr_t)b | (uintptr_t)c) & 15) == 0;
 }
-int segments(int T, int K, int W) {   // of a token, at most what keeps the grid within 31 bits
-  const int64_t n = ((int64_t)K + B_LANES * W - 1) / (B_LANES * W);
-  return (int)(n < 0x7fffffff / T ? n : 0x7fffffff / T);
-}
+int segments(int K, int W) { return (K + B_LANES * W - 1) / (B_LANES * W); }   // of a token
 
 }  // namespace
 
@@ -198,24 +195,29 @@ hipError_t launch_dispatch(const uint16_t* x, int T, int K, const int32_t* row_o
                            hipStream_t stream) {
   const bool w = wide(K, x, A);
   const int n = (int)(((int64_t)K + (w ? 15 : 1)) / (w ? 16 : 2));   // lanes of two chunks
-  const dim3 block(n >= D_LANES ? D_LANES : (n + 63) & ~63);
-  if (w)
-    hipLaunchKernelGGL(dispatch_kernel<8>, dim3(T), block, 0, stream, x, K, row_of_slot, top_k, R, A);
-  else
-    hipLaunchKernelGGL(dispatch_kernel<1>, dim3(T), block, 0, stream, x, K, row_of_slot, top_k, R, A);
-  return hipGetLastError();
+  const int lanes = n >= D_LANES ? D_LANES : (n + 63) & ~63;
+  return in_launches(T, lanes, [&](int64_t t, int64_t tokens) {
+    const dim3 grid((unsigned)tokens), block(lanes);
+    if (w)
+      hipLaunchKernelGGL(dispatch_kernel<8>, grid, block, 0, stream, x + t * K, K, row_of_slot + t * top_k, top_k, R, A);
+    else
+      hipLaunchKernelGGL(dispatch_kernel<1>, grid, block, 0, stream, x + t * K, K, row_of_slot + t * top_k, top_k, R, A);
+  });
 }
 
 hipError_t launch_dispatch_backward(const uint16_t* dA, int R, int K, const int32_t* row_of_slot, int T, int top_k,
                                     uint16_t* dx, hipStream_t stream) {
   const bool w = wide(K, dA, dx);
-  const int n = segments(T, K, w ? 8 : 1);
-  const dim3 grid((unsigned)T * (unsigned)n), block(B_LANES);
-  if (w)
-    hipLaunchKernelGGL(dispatch_backward_kernel<8>, grid, block, 0, stream, dA, R, K, row_of_slot, top_k, dx, n);
-  else
-    hipLaunchKernelGGL(dispatch_backward_kernel<1>, grid, block, 0, stream, dA, R, K, row_of_slot, top_k, dx, n);
-  return hipGetLastError();
+  const int n = segments(K, w ? 8 : 1);
+  return in_launches(T, (int64_t)n * B_LANES, [&](int64_t t, int64_t tokens) {
+    const dim3 grid((unsigned)(tokens * n)), block(B_LANES);
+    if (w)
+      hipLaunchKernelGGL(dispatch_backward_kernel<8>, grid, block, 0, stream, dA, R, K, row_of_slot + t * top_k, top_k,
+                         dx + t * K, n);
+    else
+      hipLaunchKernelGGL(dispatch_backward_kernel<1>, grid, block, 0, stream, dA, R, K, row_of_slot + t * top_k, top_k,
+                         dx + t * K, n);
+  });
 }
 
 hipError_t launch_combine_backward(const uint16_t* C, const uint16_t* dout, int R, int N, const int32_t* row_of_slot,
@@ -223,14 +225,16 @@ hipError_t launch_combine_backward(const uint16_t* C, const uint16_t* dout, int 
                                    hipStream_t stream) {
   const int64_t slots = (int64_t)T * top_k;
   constexpr int per_wg = C_WAVES / C_SPLIT;
-  const dim3 grid((unsigned)((slots + per_wg * 32 - 1) / (per_wg * 32) * 32)), block(64 * C_WAVES);   // see b
-  if (wide(N, C, dout, dC))
-    hipLaunchKernelGGL(combine_backward_kernel<8>, grid, block, 0, stream, C, dout, R, N, row_of_slot, weights, slots,
-                       top_k, dC, dweights);
-  else
-    hipLaunchKernelGGL(combine_backward_kernel<1>, grid, block, 0, stream, C, dout, R, N, row_of_slot, weights, slots,
-                       top_k, dC, dweights);
-  return hipGetLastError();
+  // launches of a multiple of 64 slots: whole sets of 32 workgroups (see b)
+  return in_launches(slots, 64 * C_SPLIT, [&](int64_t s, int64_t n) {
+    const dim3 grid((unsigned)((n + per_wg * 32 - 1) / (per_wg * 32) * 32)), block(64 * C_WAVES);
+    if (wide(N, C, dout, dC))
+      hipLaunchKernelGGL(combine_backward_kernel<8>, grid, block, 0, stream, C, dout, R, N, row_of_slot, weights, s,
+                         slots, top_k, dC, dweights);
+    else
+      hipLaunchKernelGGL(combine_backward_kernel<1>, grid, block, 0, stream, C, dout, R, N, row_of_slot, weights, s,
+                         slots, top_k, dC, dweights);
+  });
 }
 
 }  // namespace w4a8

@@ -29,6 +29,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 namespace w4a8 {
 namespace {
 
@@ -503,32 +505,47 @@ gate_backward_kernel(const void* __restrict__ logits, int E, const int32_t* __re
     ROW(24)                                                                                                   \
   }
 
-unsigned narrow_grid(int T, int W) { return (unsigned)(((int64_t)T * W + 64 * ROWS_PER_WG - 1) / (64 * ROWS_PER_WG)); }
+unsigned narrow_grid(int64_t T, int W) { return (unsigned)((T * W + 64 * ROWS_PER_WG - 1) / (64 * ROWS_PER_WG)); }
 unsigned row_threads(int E, int V) { return 64u * ((E + 64 * V - 1) / (64 * V)); }
+template <bool BF16, typename P>
+P* row_of(P* logits, int64_t t, int E) {
+  typedef typename std::conditional<std::is_const<P>::value, const char, char>::type Byte;
+  return (Byte*)logits + (size_t)t * E * (BF16 ? 2 : 4);
+}
 
 template <bool BF16>
-void launch_fwd(const void* logits, int T, int E, int k, int score, int renorm, float scale, int32_t* ids,
-                float* weights, hipStream_t st) {
-#define NARROW(W)                                                                                                  \
-  hipLaunchKernelGGL((gate_narrow_kernel<W, BF16>), dim3(narrow_grid(T, W)), dim3(64 * ROWS_PER_WG), 0, st, logits, \
-                     T, E, k, score, renorm, scale, ids, weights);
-#define ROW(V)                                                                                                    \
-  hipLaunchKernelGGL((gate_kernel<V, BF16>), dim3(T), dim3(row_threads(E, V)), 0, st, logits, E, k, score, renorm, \
-                     scale, ids, weights);
+hipError_t launch_fwd(const void* logits, int T, int E, int k, int score, int renorm, float scale, int32_t* ids,
+                      float* weights, hipStream_t st) {
+#define NARROW(W)                                                                                                \
+  return in_launches(T, W, [&](int64_t t, int64_t n) {                                                           \
+    hipLaunchKernelGGL((gate_narrow_kernel<W, BF16>), dim3(narrow_grid(n, W)), dim3(64 * ROWS_PER_WG), 0, st,    \
+                       row_of<BF16>(logits, t, E), (int)n, E, k, score, renorm, scale, ids + t * k, weights + t * k); \
+  });
+#define ROW(V)                                                                                                   \
+  return in_launches(T, row_threads(E, V), [&](int64_t t, int64_t n) {                                           \
+    hipLaunchKernelGGL((gate_kernel<V, BF16>), dim3((unsigned)n), dim3(row_threads(E, V)), 0, st,                \
+                       row_of<BF16>(logits, t, E), E, k, score, renorm, scale, ids + t * k, weights + t * k);    \
+  });
   W4A8_GATE_ROWS(NARROW, ROW)
 #undef NARROW
 #undef ROW
 }
 
 template <bool BF16>
-void launch_bwd(const void* logits, int T, int E, const int32_t* ids, const float* dweights, int k, int score,
-                int renorm, float scale, void* dlogits, hipStream_t st) {
-#define NARROW(W)                                                                                            \
-  hipLaunchKernelGGL((gate_backward_narrow_kernel<W, BF16>), dim3(narrow_grid(T, W)), dim3(64 * ROWS_PER_WG), 0, st, \
-                     logits, T, E, ids, dweights, k, score, renorm, scale, dlogits);
-#define ROW(V)                                                                                                     \
-  hipLaunchKernelGGL((gate_backward_kernel<V, BF16>), dim3(T), dim3(row_threads(E, V)), 0, st, logits, E, ids,      \
-                     dweights, k, score, renorm, scale, dlogits);
+hipError_t launch_bwd(const void* logits, int T, int E, const int32_t* ids, const float* dweights, int k, int score,
+                      int renorm, float scale, void* dlogits, hipStream_t st) {
+#define NARROW(W)                                                                                                \
+  return in_launches(T, W, [&](int64_t t, int64_t n) {                                                           \
+    hipLaunchKernelGGL((gate_backward_narrow_kernel<W, BF16>), dim3(narrow_grid(n, W)), dim3(64 * ROWS_PER_WG), 0, st, \
+                       row_of<BF16>(logits, t, E), (int)n, E, ids + t * k, dweights + t * k, k, score, renorm, scale, \
+                       row_of<BF16>(dlogits, t, E));                                                             \
+  });
+#define ROW(V)                                                                                                   \
+  return in_launches(T, row_threads(E, V), [&](int64_t t, int64_t n) {                                           \
+    hipLaunchKernelGGL((gate_backward_kernel<V, BF16>), dim3((unsigned)n), dim3(row_threads(E, V)), 0, st,       \
+                       row_of<BF16>(logits, t, E), E, ids + t * k, dweights + t * k, k, score, renorm, scale,    \
+                       row_of<BF16>(dlogits, t, E));                                                             \
+  });
   W4A8_GATE_ROWS(NARROW, ROW)
 #undef NARROW
 #undef ROW
@@ -539,21 +556,15 @@ void launch_bwd(const void* logits, int T, int E, const int32_t* ids, const floa
 
 hipError_t launch_topk_gate(const void* logits, bool bf16, int T, int E, int k, int score, int renorm, float scale,
                             int32_t* ids, float* weights, hipStream_t stream) {
-  if (bf16)
-    launch_fwd<true>(logits, T, E, k, score, renorm, scale, ids, weights, stream);
-  else
-    launch_fwd<false>(logits, T, E, k, score, renorm, scale, ids, weights, stream);
-  return hipGetLastError();
+  if (bf16) return launch_fwd<true>(logits, T, E, k, score, renorm, scale, ids, weights, stream);
+  return launch_fwd<false>(logits, T, E, k, score, renorm, scale, ids, weights, stream);
 }
 
 hipError_t launch_topk_gate_backward(const void* logits, bool bf16, int T, int E, const int32_t* ids,
                                      const float* dweights, int k, int score, int renorm, float scale, void* dlogits,
                                      hipStream_t stream) {
-  if (bf16)
-    launch_bwd<true>(logits, T, E, ids, dweights, k, score, renorm, scale, dlogits, stream);
-  else
-    launch_bwd<false>(logits, T, E, ids, dweights, k, score, renorm, scale, dlogits, stream);
-  return hipGetLastError();
+  if (bf16) return launch_bwd<true>(logits, T, E, ids, dweights, k, score, renorm, scale, dlogits, stream);
+  return launch_bwd<false>(logits, T, E, ids, dweights, k, score, renorm, scale, dlogits, stream);
 }
 
 }  // namespace w4a8

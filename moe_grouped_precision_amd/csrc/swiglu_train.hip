@@ -164,23 +164,33 @@ swiglu_backward_kernel(const uint8_t* __restrict__ codes, const float* __restric
 hipError_t launch_swiglu(const uint16_t* C, int R, int I, uint16_t* h, uint8_t* codes, float* scales,
                          hipStream_t stream) {
   const int G = I >> 7, blocks = (G + S_GROUPS - 1) / S_GROUPS;
-  const dim3 grid((unsigned)R * (unsigned)blocks), block(16 * (G < S_GROUPS ? G : S_GROUPS));
-  if (codes)
-    hipLaunchKernelGGL(swiglu_kernel<true>, grid, block, 0, stream, C, blocks, I, h, codes, scales);
-  else
-    hipLaunchKernelGGL(swiglu_kernel<false>, grid, block, 0, stream, C, blocks, I, h, codes, scales);
-  return hipGetLastError();
+  const int threads = 16 * (G < S_GROUPS ? G : S_GROUPS);
+  return in_launches(R, (int64_t)blocks * threads, [&](int64_t r, int64_t n) {
+    const dim3 grid((unsigned)(n * blocks)), block(threads);
+    const uint16_t* c = C + r * 2 * I;
+    if (codes)
+      hipLaunchKernelGGL(swiglu_kernel<true>, grid, block, 0, stream, c, blocks, I, h + r * I, codes + r * 2 * I,
+                         scales + r * 2 * G);
+    else
+      hipLaunchKernelGGL(swiglu_kernel<false>, grid, block, 0, stream, c, blocks, I, h + r * I, codes, scales);
+  });
 }
 
 hipError_t launch_swiglu_backward(const uint8_t* codes, const float* scales, const uint16_t* dh, int R, int I,
                                   uint16_t* dC, uint16_t* h, hipStream_t stream) {
   const int G = I >> 7, blocks = (G + S_GROUPS - 1) / S_GROUPS;
-  const dim3 grid((unsigned)R * (unsigned)blocks), block(16 * (G < S_GROUPS ? G : S_GROUPS));
-  if (h)
-    hipLaunchKernelGGL(swiglu_backward_kernel<true>, grid, block, 0, stream, codes, scales, dh, blocks, I, dC, h);
-  else
-    hipLaunchKernelGGL(swiglu_backward_kernel<false>, grid, block, 0, stream, codes, scales, dh, blocks, I, dC, h);
-  return hipGetLastError();
+  const int threads = 16 * (G < S_GROUPS ? G : S_GROUPS);
+  return in_launches(R, (int64_t)blocks * threads, [&](int64_t r, int64_t n) {
+    const dim3 grid((unsigned)(n * blocks)), block(threads);
+    const uint8_t* q = codes + r * 2 * I;
+    const float* s = scales + r * 2 * G;
+    if (h)
+      hipLaunchKernelGGL(swiglu_backward_kernel<true>, grid, block, 0, stream, q, s, dh + r * I, blocks, I,
+                         dC + r * 2 * I, h + r * I);
+    else
+      hipLaunchKernelGGL(swiglu_backward_kernel<false>, grid, block, 0, stream, q, s, dh + r * I, blocks, I,
+                         dC + r * 2 * I, h);
+  });
 }
 
 }  // namespace w4a8

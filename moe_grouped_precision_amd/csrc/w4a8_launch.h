@@ -1,5 +1,5 @@
 // Host-side launch interface between the C ABI layer (api.cpp) and the kernel
-// translation units (prep.hip, gemm.hip).
+// translation units.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -49,6 +49,22 @@ hipError_t launch_grouped_gemm_a16(const uint16_t* A, const uint8_t* B, const ui
                                    hipStream_t stream);
 hipError_t launch_quant_gather(const uint16_t* x, int T, int K, const int32_t* row_of_slot, int top_k, int R,
                                uint8_t* A, float* SA, int layout, hipStream_t stream);
+
+// A launch may have fewer than 2^32 threads per dimension; one with more is
+// cut to their number modulo 2^32, without an error.  n items of `threads`
+// threads each therefore go in as many launches as it takes: launch(first
+// item, number of items), half the limit at most in one.
+constexpr int64_t MAX_THREADS = (int64_t)1 << 31;
+template <typename F>
+hipError_t in_launches(int64_t n, int64_t threads, F launch) {
+  const int64_t most = MAX_THREADS / threads;
+  for (int64_t i = 0; i < n; i += most) {
+    launch(i, n - i < most ? n - i : most);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
 
 hipError_t launch_topk_gate(const void* logits, bool bf16, int T, int E, int k, int score, int renorm, float scale,
                             int32_t* ids, float* weights, hipStream_t stream);
