@@ -133,7 +133,7 @@ swiglu_backward_kernel(const uint8_t* __restrict__ codes, const float* __restric
   decode8(codes + at, fg);
   decode8(codes + at + I, fu);
   load8(dh + hat, fd);
-  float dg[8], du[8], hh[8];
+  float dg[8], du[8], hh[8], slope[8], most = 0.f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     // g = code * q needs 28 bits: what fp32 cuts off it (lo) would cost |g|
@@ -146,13 +146,18 @@ swiglu_backward_kernel(const uint8_t* __restrict__ codes, const float* __restric
     const float x0 = exp_f32(fminf(-gv, 88.0f));
     const float x = fabsf(gv) < 104.0f ? fmaf(-x0, lo, x0) : x0;
     const float s = gv <= -104.0f ? 0.0f : __builtin_amdgcn_rcpf(1.0f + x);
-    const float silu = gv * s, slope = s * fmaf(gv, x * s, 1.0f);
-    // dh u first (u slope may underflow under a large dh); where that leaves
-    // fp32, slope (at most 1.1) goes in between
-    const float du_dh = fd[e] * uv;
-    dg[e] = fabsf(du_dh) < __builtin_inff() ? du_dh * slope : fd[e] * (uv * slope);
+    const float silu = gv * s, prod = fd[e] * uv;
+    slope[e] = s * fmaf(gv, x * s, 1.0f);
+    most = fmaxf(most, fabsf(prod));
+    dg[e] = prod * slope[e];
     du[e] = fd[e] * silu;
     hh[e] = silu * uv;
+  }
+  // dh u first (u slope may underflow under a large dh); where that left fp32,
+  // slope (at most 1.1) goes in between
+  if (__builtin_expect(most == __builtin_inff(), 0)) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dg[e] = fabsf(fd[e] * (fu[e] * qu)) < __builtin_inff() ? dg[e] : fd[e] * (fu[e] * qu * slope[e]);
   }
   store8(dC + at, dg);
   store8(dC + at + I, du);
