@@ -72,8 +72,10 @@ hipError_t launch_combine(const uint16_t* C, int R, int N, const int32_t* row_of
   // one 16-byte chunk per lane, whole waves, at most 512 lanes
   const int chunks = N / 8;
   const int threads = chunks >= 512 ? 512 : ((chunks + 63) & ~63);
-  hipLaunchKernelGGL(combine_kernel, dim3(T), dim3(threads), 0, stream, C, R, N, row_of_slot, weights, top_k, out);
-  return hipGetLastError();
+  return in_launches(T, threads, [&](int64_t t, int64_t n) {
+    hipLaunchKernelGGL(combine_kernel, dim3((unsigned)n), dim3(threads), 0, stream, C, R, N, row_of_slot + t * top_k,
+                       weights + t * top_k, top_k, out + t * N);
+  });
 }
 
 }  // namespace w4a8

@@ -108,9 +108,11 @@ quant_gather_kernel(const uint16_t* __restrict__ x, int K, const int32_t* __rest
 __global__ void __launch_bounds__(512)
 swiglu_quant_kernel(const uint16_t* __restrict__ C, int R, int I, uint8_t* __restrict__ A, float* __restrict__ SA,
                     int layout) {
-  // M-major scales: consecutive rows on one XCD (see quant_gather_kernel)
-  const int r = (layout == 0 || (R & 7)) ? (int)blockIdx.x
-                                         : (int)((blockIdx.x & 7) * (R >> 3) + (blockIdx.x >> 3));
+  // M-major scales: consecutive rows on one XCD (see quant_gather_kernel); the
+  // launch has gridDim.x of the R rows
+  const int n = gridDim.x;
+  const int r = (layout == 0 || (n & 7)) ? (int)blockIdx.x
+                                         : (int)((blockIdx.x & 7) * (n >> 3) + (blockIdx.x >> 3));
   const int G = I >> 7;
   const int lane8 = threadIdx.x & 7;
   const int gsub = threadIdx.x >> 3;
@@ -154,8 +156,10 @@ hipError_t launch_swiglu_quant(const uint16_t* C, int R, int I, uint8_t* A, floa
   if (R == 0) return hipSuccess;
   const int G = I >> 7;
   const int threads = 8 * (G < 64 ? ((G + 7) & ~7) : 64);
-  hipLaunchKernelGGL(swiglu_quant_kernel, dim3(R), dim3(threads), 0, stream, C, R, I, A, SA, layout);
-  return hipGetLastError();
+  return in_launches(R, threads, [&](int64_t r, int64_t n) {
+    hipLaunchKernelGGL(swiglu_quant_kernel, dim3((unsigned)n), dim3(threads), 0, stream, C + r * 2 * I, R, I, A + r * I,
+                       layout ? SA + r : SA + r * G, layout);
+  });
 }
 
 hipError_t launch_quant_gather(const uint16_t* x, int T, int K, const int32_t* row_of_slot, int top_k, int R,
@@ -165,9 +169,10 @@ hipError_t launch_quant_gather(const uint16_t* x, int T, int K, const int32_t* r
   // whole number of waves)
   const int G = K >> 7;
   const int threads = 8 * (G < 64 ? ((G + 7) & ~7) : 64);
-  hipLaunchKernelGGL(quant_gather_kernel, dim3(T), dim3(threads), 0, stream, x, K, row_of_slot, top_k, R, A, SA,
-                     layout);
-  return hipGetLastError();
+  return in_launches(T, threads, [&](int64_t t, int64_t n) {
+    hipLaunchKernelGGL(quant_gather_kernel, dim3((unsigned)n), dim3(threads), 0, stream, x + t * K, K,
+                       row_of_slot + t * top_k, top_k, R, A, SA, layout);
+  });
 }
 
 }  // namespace w4a8
