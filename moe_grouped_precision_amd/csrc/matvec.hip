@@ -17,6 +17,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 
 namespace w4a8 {
 namespace {
@@ -611,10 +612,21 @@ constexpr int MV_LDS = 160 * 1024;   // of a CU
 
 template <int FMT, int GROUP, int TB, int WAVES>
 hipError_t launch_path(const MatvecArgs& a, int rows, int grid, int lds, hipStream_t stream) {
-  if (lds > 64 * 1024) {   // past what a launch may have without asking
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&matvec_kernel<FMT, GROUP, TB, WAVES>),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  if (lds > 64 * 1024) {
+    // Past what a launch may have without asking: the kernel may have all of a
+    // CU's LDS from its first such call on a device on.  One amount for every
+    // call, so that no host thread lowers it between another's request and launch.
+    static std::atomic<uint64_t> allowed{0};   // a bit per device
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
     if (e != hipSuccess) return e;
+    const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+    if (!(allowed.load(std::memory_order_acquire) & bit)) {
+      e = hipFuncSetAttribute(reinterpret_cast<const void*>(&matvec_kernel<FMT, GROUP, TB, WAVES>),
+                              hipFuncAttributeMaxDynamicSharedMemorySize, MV_LDS);
+      if (e != hipSuccess) return e;
+      allowed.fetch_or(bit, std::memory_order_release);
+    }
   }
   hipLaunchKernelGGL((matvec_kernel<FMT, GROUP, TB, WAVES>), dim3(grid), dim3(64 * WAVES), lds, stream, a, rows);
   return hipGetLastError();
