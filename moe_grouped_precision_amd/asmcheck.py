@@ -1,17 +1,22 @@
 """Static check of the gfx950 assembly that hipcc generates for the kernels.
 
-    python -m moe_grouped_precision_amd.asmcheck <file.s>
+    python -m moe_grouped_precision_amd.asmcheck [--lds] <file.s>
 
 The GEMM kernels issue their K-loop vector-memory operations as inline asm
 and wait for them with explicit ``s_waitcnt vmcnt``; the compiler does not
 see those loads.  This check proves, over the control-flow graph of every
-kernel, two properties the compiler can no longer guarantee by itself:
+kernel, what the compiler can no longer guarantee by itself:
 
 * no instruction reads or overwrites a VGPR that a still-pending vector-memory
   load may write (loads complete in issue order, so after ``vmcnt(N)`` only
   the N newest operations can be pending);
 * every vector-memory instruction that takes a scalar (SGPR) address operand
-  is at least 5 wait states after the last VALU write of that SGPR.
+  is at least 5 wait states after the last VALU write of that SGPR;
+* with ``lds=True``, no LDS read and no barrier while a load from memory
+  straight to LDS may be pending: its wait, a ``vmcnt(N)`` that leaves N newer
+  operations in flight, has N of them behind it on every path.  (For kernels
+  that fill LDS once.  A kernel that keeps such loads in flight across
+  barriers on purpose is checked by its own counts, not by this rule.)
 
 The dataflow is conservative: at a merge point a register is pending if it
 may be pending on any incoming path.  Long branches (s_getpc_b64 / add /
@@ -30,7 +35,8 @@ _VREG = re.compile(r"\bv\[(\d+):(\d+)\]|\bv(\d+)\b")
 _SPAIR = re.compile(r"\bs\[(\d+):(\d+)\]")
 _SREG = re.compile(r"\bs\[(\d+):(\d+)\]|\bs(\d+)\b")
 _BRANCH = re.compile(r"^s_(c?branch\w*)\s+(\S+)")
-_MAXQ = 64
+_MAXQ = 64   # a wave has at most 63 operations in flight
+_TO_LDS = -1  # in place of a destination register: a load straight to LDS
 
 
 def _vregs(text):
@@ -130,7 +136,7 @@ def _is_vmem(op):
     return op.startswith(("global_", "buffer_", "scratch_", "flat_"))
 
 
-def _check_kernel(kern, findings):
+def _check_kernel(kern, findings, lds=False):
     nb = len(kern["blocks"])
     state_in = [None] * nb
     state_in[0] = []
@@ -160,6 +166,10 @@ def _check_kernel(kern, findings):
                 continue
             ops = [x.strip() for x in rest.split(",")] if rest.strip() else []
             pend = set().union(*q) if q else set()
+            if lds and _TO_LDS in pend and (op == "s_barrier" or op.startswith(("ds_read", "ds_load"))) and (
+                    (no, "l") not in reported):
+                reported.add((no, "l"))
+                findings.append(f"line {no}: {text}: with a load to LDS pending")
             if _is_vmem(op):
                 loads_reg = ("load" in op) and ("_lds" not in op) and not re.search(r"\blds\b", rest)
                 dst = _vregs(ops[0]) if (loads_reg and ops) else set()
@@ -175,6 +185,8 @@ def _check_kernel(kern, findings):
                             reported.add((no, "s"))
                             findings.append(f"line {no}: {text}: SGPR s{r} written by VALU "
                                             f"{count - last_valu_sgpr[r] - 1} wait states before")
+                if "load" in op and not loads_reg:
+                    dst = {_TO_LDS}
                 q.insert(0, dst)
                 q = q[:_MAXQ]
                 continue
@@ -215,7 +227,7 @@ def _unreached(kern):
     return [b for b in range(len(kern["blocks"])) if b not in seen and kern["blocks"][b]["ins"]]
 
 
-def check(path: str):
+def check(path: str, lds: bool = False):
     lines = open(path).read().split("\n")
     findings = []
     for kern in _parse(lines):
@@ -226,12 +238,12 @@ def check(path: str):
             b = kern["blocks"][un[0]]
             findings.append(f"{kern['name']}: {len(un)} block(s) unreachable in the parsed CFG, first at line "
                             f"{b['ins'][0][0]} -- the check would not cover them")
-        _check_kernel(kern, findings)
+        _check_kernel(kern, findings, lds)
     return findings
 
 
 if __name__ == "__main__":
-    found = check(sys.argv[1])
+    found = check(sys.argv[-1], lds="--lds" in sys.argv[1:-1])
     for f in found[:50]:
         print(f)
     print(f"{len(found)} finding(s)")
