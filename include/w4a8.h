@@ -427,7 +427,7 @@ int w4a8_topk_gate(const void* logits_dev, int logits_type, int T, int E, int to
  * dlogits_dev  out [T][E] in the logits' type, every element written: zero
  *              outside the selection, except that softmax without renorm
  *              reaches every expert with a finite logit.  fp32 inside, one
- *              rounding.
+ *              rounding.  Must not overlap the logits.
  * Limits and alignment as w4a8_topk_gate.
  */
 int w4a8_topk_gate_backward(const void* logits_dev, int logits_type, int T, int E, const int32_t* ids_dev,
@@ -546,7 +546,8 @@ int w4a8_swiglu(const uint16_t* C_bf16_dev, int R, int I, uint16_t* h_bf16_dev, 
  * w4a8_swiglu kept: with g, u the copy's values (code * s) and s = 1 / (1 +
  * e^-g),
  *   dC[:, :I] = bf16_rne(dh * u * s * (1 + g * (1 - s))),
- *   dC[:, I:] = bf16_rne(dh * g * s),   h = bf16_rne(g * s * u).
+ *   dC[:, I:] = bf16_rne(dh * g * s),   h = bf16_rne(g * s * u),
+ * in fp32: s counts as 0 from g = -104 down, where it is below fp32's range.
  *
  * ckpt_fp8_dev, ckpt_scales_dev: as w4a8_swiglu wrote them.
  * dh_bf16_dev  bf16 [R][I].

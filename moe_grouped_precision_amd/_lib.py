@@ -484,7 +484,8 @@ def topk_gate(logits: torch.Tensor, top_k: int, score: int = GATE_SOFTMAX, renor
 def topk_gate_backward(logits: torch.Tensor, ids: torch.Tensor, dweights: torch.Tensor, score: int = GATE_SOFTMAX,
                        renorm: bool = True, scale: float = 1.0, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """dlogits [T, E] (the logits' type) from dweights fp32 [T, top_k]; logits,
-    score, renorm and scale as given to topk_gate, ids as it returned them."""
+    score, renorm and scale as given to topk_gate, ids as it returned them.
+    out must not be the logits."""
     lib = load()
     kind = _logits_type(logits)
     T, E = logits.shape

@@ -93,7 +93,7 @@ dispatch_kernel(const uint16_t* __restrict__ x, int K, const int32_t* __restrict
 }
 
 // One workgroup per token and 256 chunks, so that the last round of
-// workgroups is short (1151 tokens x 6144, top-8: 22.3 us, 5.5 TB/s; 25.1
+// workgroups is short (1151 tokens x 6144, top-8: 22.8 us, 5.3 TB/s; 25.1
 // with a workgroup per token).  Nontemporal loads: 25.5 without.
 constexpr int B_LANES = 256;
 template <int W>

@@ -22,8 +22,11 @@
 //
 // What it measured in the kernel: 64 x 32 3.0 us and the gradient of 16384 x
 // 32 4.7 us, both at the length of a launch and one trip to memory; 2047 x
-// 6144 bf16 9.4 to 10.8 us (25 MB: 2.5 TB/s), bound by the three barriers of
-// a row and the rounds of a maximum between them, with 8 rows on a CU.
+// 6144 bf16 9.4 to 10.8 us (25 MB: 2.5 TB/s; 17 us for the softmax over all),
+// bound by the three barriers of a row and the rounds of a maximum between
+// them, with 8 rows on a CU.  The gradient of 2047 x 6144 bf16, a call: 12.6
+// us for the sigmoid (25 MB written, only the selected logits read), 20.8 us
+// for the softmax over all (50 MB: 2.4 TB/s).
 #include "swiglu.h"
 #include "w4a8_launch.h"
 

@@ -7,8 +7,10 @@
 // INT4: q a code 0 .. 15, z its zero point (8 when none are given), s bf16
 // per 32, 64 or 128 K.  No zero point for the first two.
 //
-// Bound by the weights' bytes: every expert that some slot names is read
-// once, whatever the number of its slots.  matvec_kernel (below) is the path;
+// Bound by the weights' bytes: an expert that some slot names is read once per
+// item, up to 16 of its slots (launch_waves: at most twice the mean number of
+// slots per expert, at least four), so slots that crowd on few experts read
+// these more than once.  matvec_kernel (below) is the path;
 // matvec_plain_kernel serves rows shorter than one of its steps, rows that do
 // not fit in LDS and experts of 4 GB and more.
 #include "w4a8_device.h"
@@ -128,10 +130,13 @@ matvec_plain_kernel(const MatvecArgs a) {
 // K in steps of 256 (wave w takes steps w, w + waves, ...) and join their
 // sums in LDS.
 //
-// What it measured (weights not in the caches): 8 experts 4096 x 6144, one
-// token, MXFP4 19.4 us (107 MB: 5.5 TB/s), NVFP4 20.7, INT4 per 128 22.3; 64
-// slots of 32 such experts 65 us (386 MB: 5.9 TB/s); 65536 x 6144 dense 35.8
-// us (214 MB: 6.0 TB/s).  Bound by HBM, after 3 to 4 us of start (ids, x and
+// What it measured (calls in a row, weights not in the caches): 8 experts
+// 4096 x 6144, one token, MXFP4 18.7 us (107 MB: 5.7 TB/s; alone in a trace
+// 20.5), NVFP4 20.0, INT4 per 128 21.0; 64 slots of 32 such experts 64 us (386
+// MB: 6.0 TB/s), all 64 on one expert 30 us (13 MB, read by sixteen items,
+// mostly from the caches), INT4 37; 65536 x 6144 dense 34.2 us (214 MB: 6.3
+// TB/s); 6144 x 6144 dense, 17, 32 and 64 rows: MXFP4 11, 16 and 24 us, INT4
+// 21, 32 and 53.  Bound by HBM, after 3 to 4 us of start (ids, x and
 // the first weights, each a trip to memory, and code read for the first time
 // in the launch).  Four steps in registers instead of three: 2% more on the
 // long shapes, 10% less on one row of 6144 x 6144 (more code); four
@@ -675,8 +680,8 @@ hipError_t launch_matvec(const MatvecArgs& a, int cus, hipStream_t stream) {
   // Eight waves where a CU gets one workgroup in any case: not enough units
   // for two (one row of 2048 x 6144, MXFP4: 8.6 against 10.3 us with four, 5
   // rows of 3583 x 6144, INT4: 10.8 against 11.2), or so many rows of x that
-  // the LDS holds no second (16 rows of 6144 x 6144: MXFP4 12.4 against 14.0
-  // us, INT4 22.5 against 23.8, NVFP4 17.6 against 17.3).  Else four (24 slots
+  // the LDS holds no second (16 rows of 6144 x 6144: MXFP4 10.4 against 12.9
+  // us, INT4 20.3 against 22.0, NVFP4 15.1 against 16.1).  Else four (24 slots
   // of 6144 x 2048: NVFP4 25.8 against 27.4 us, INT4 28.0 against 32.9).
   const int64_t units = (int64_t)std::min(a.S, a.E) * ((a.N + 15) / 16);
   if (units <= cus || (!a.ids && a.S > 8)) return launch_waves<8>(a, cus, units, stream);

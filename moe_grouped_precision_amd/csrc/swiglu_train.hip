@@ -11,9 +11,10 @@
 // A stream: 16 lanes per 128 columns of g and the same of u, 8 columns of each
 // per lane (16-byte loads, consecutive lanes), the group maxima by DPP
 // rotations; no LDS, no barrier.  Bound by HBM's mix of reads and writes: 9216
-// rows of I = 2048 with the copy 26.3 us in the kernel (152 MB: 5.8 TB/s), the
-// gradient with h 32.2 us (189 MB: 5.9 TB/s); a plain copy of large buffers
-// runs at 4.7.  8 lanes per group with two loads each took 30.6 and 37.7 us,
+// rows of I = 2048 with the copy 26.0 us in the kernel (152 MB: 5.8 TB/s), the
+// gradient with h 32.7 us (190 MB: 5.8 TB/s); a plain copy of large buffers
+// runs at 4.7.  I = 2176, whose rows take a workgroup of 16 groups and one of
+// a single group: 39 and 47 us a call (4.1 and 4.3 TB/s).  8 lanes per group with two loads each took 30.6 and 37.7 us,
 // a 64-bit division per lane 1% more.
 #include "swiglu.h"
 #include "w4a8_launch.h"
