@@ -64,14 +64,14 @@ enum {
   W4A8_SCALE_M_MAJOR = 1    /* a_scales fp32 [K/128][R]: SA(r,g) at g*R+r, R = offsets[E] */
 };
 
-/* Weight-scale formats of w4a8_grouped_gemm_a16 (the first two) and w4a8_matvec. */
+/* Weight-scale formats of w4a8_grouped_gemm_a16 and w4a8_quantize_fp4 (the first two) and w4a8_matvec. */
 enum {
   W4A8_WSCALE_MX = 0,  /* MXFP4: E8M0 code per (expert, column, 32 K), value 2^(code-127) */
   W4A8_WSCALE_NV = 1,  /* NVFP4: E4M3FN code per (expert, column, 16 K) */
   W4A8_WSCALE_INT4 = 2 /* codes 0..15 with a bf16 scale per (expert, column, 32, 64 or 128 K) */
 };
 
-/* Types of the router's logits. */
+/* Types of the router's logits, of norm weights, weight gradients and clipped tensors. */
 enum { W4A8_TYPE_F32 = 0, W4A8_TYPE_BF16 = 1 };
 
 /* Scores of the router's gate. */
@@ -558,6 +558,199 @@ int w4a8_swiglu(const uint16_t* C_bf16_dev, int R, int I, uint16_t* h_bf16_dev, 
  */
 int w4a8_swiglu_backward(const uint8_t* ckpt_fp8_dev, const float* ckpt_scales_dev, const uint16_t* dh_bf16_dev,
                          int R, int I, uint16_t* dC_bf16_dev, uint16_t* h_bf16_dev, void* stream);
+
+/*
+ * w4a8_rms_norm -- root-mean-square norm in front of the experts, with the
+ * residual's addition and the output in bf16, in 8 bits, or both:
+ *   h[t, :] = bf16_rne(x[t, :] + residual[t, :])   (the sum in fp32; h = x without a residual)
+ *   y[t, k] = h[t, k] * (sum over k of h[t, k]^2 / K + eps)^(-1/2) * weight[k]   (fp32)
+ *   y_bf16  = bf16_rne(y)
+ *   per (row, 128 columns): s = amax|y| / 448 (1 where amax < 2^-100), code =
+ *   E4M3FN round-to-nearest-even of y * (1/s): the input of w4a8_grouped_gemm.
+ * The norm is of h as it is stored, so that the next layer and the backward
+ * pass see the values it was taken of.
+ *
+ * x_bf16_dev         bf16 [T][K].
+ * residual_bf16_dev  bf16 [T][K] or NULL.
+ * weight_dev, weight_type: [K] of W4A8_TYPE_F32 or W4A8_TYPE_BF16, or NULL for ones.
+ * y_bf16_dev         out bf16 [T][K] or NULL.
+ * sum_bf16_dev       out bf16 [T][K], h, or NULL.
+ * A_fp8_dev, a_scales_dev, a_scale_layout: out uint8 [T][K] codes and fp32
+ *                    scales in the layouts of w4a8_grouped_gemm (R = T), or both NULL.
+ * At least one of y and A is asked for.  y and sum may be the buffers of x or
+ * of the residual (not y and sum the same one); otherwise no output overlaps
+ * an input or another output.
+ * Sums are taken in 64 bits and any finite row has its value (no overflow of
+ * the squares).  Rows of zeros with eps = 0, and rows with an infinity or a
+ * NaN, are what the formula gives (NaN, or 0 beside an infinity); a group of
+ * codes with an infinity reads back as NaN.
+ * Limits: T >= 0, 1 <= K <= W4A8_MAX_K, K % 128 == 0 with codes, eps >= 0.
+ * T == 0 does nothing.  bf16 buffers need 2-byte, fp32 ones 4-byte, A 16-byte
+ * alignment; with K % 8 == 0 and 16-byte alignment rows move 16 bytes at a time.
+ */
+int w4a8_rms_norm(const uint16_t* x_bf16_dev, const uint16_t* residual_bf16_dev, const void* weight_dev,
+                  int weight_type, int T, int K, float eps, uint16_t* y_bf16_dev, uint16_t* sum_bf16_dev,
+                  uint8_t* A_fp8_dev, float* a_scales_dev, int a_scale_layout, void* stream);
+
+/*
+ * w4a8_rms_norm_backward -- its gradient at h: with n = (sum h^2 / K + eps)^(-1/2)
+ * of the row, g = dy * weight,
+ *   dx[t, k] = bf16_rne(n * (g[k] - h[k] n * sum over j of g[j] h[j] n / K) + dsum[t, k])
+ *   dweight[k] = sum over t of dy[t, k] * h[t, k] * n   (fp32)
+ * dx is the gradient of both x and the residual.
+ *
+ * h_bf16_dev     bf16 [T][K], the forward call's sum (its x without a residual).
+ * dy_bf16_dev    bf16 [T][K].
+ * dsum_bf16_dev  bf16 [T][K] or NULL: the gradient that reaches h beside y.
+ * dx_bf16_dev    out bf16 [T][K]; may be the buffer of dy, dsum or h.
+ * dweight_dev    out fp32 [K], or NULL.
+ * workspace_dev  w4a8_rms_norm_backward_bytes(T, K) bytes, 4-byte aligned, not
+ *                shared by calls that may run at a time.
+ * Every run gives the same bits.  Limits and alignment as w4a8_rms_norm.
+ * T == 0 writes zeros to dweight.
+ */
+int w4a8_rms_norm_backward(const uint16_t* h_bf16_dev, const void* weight_dev, int weight_type,
+                           const uint16_t* dy_bf16_dev, const uint16_t* dsum_bf16_dev, int T, int K, float eps,
+                           uint16_t* dx_bf16_dev, float* dweight_dev, void* workspace_dev, size_t workspace_bytes,
+                           void* stream);
+
+/* Workspace of w4a8_rms_norm_backward; 0 for sizes it refuses and for T == 0. */
+size_t w4a8_rms_norm_backward_bytes(int T, int K);
+
+/*
+ * w4a8_grouped_gemm_bf16 -- the products grouped by expert with bf16 weights,
+ * for experts that are trained, and both gradients:
+ *   w4a8_grouped_gemm_bf16    C[r, n]     = bf16_rne(sum over k of A[r, k] * W[e, n, k])
+ *   w4a8_grouped_gemm_dgrad   dA[r, k]    = bf16_rne(sum over n of dC[r, n] * W[e, n, k])
+ *   w4a8_grouped_gemm_wgrad   dW[e, n, k] = sum over the rows r of e of dC[r, n] * A[r, k]
+ * with e the expert of offsets[e] <= r < offsets[e+1], sums in fp32.
+ *
+ * A_bf16_dev          bf16 [R][K], dC_bf16_dev bf16 [R][N], W_bf16_dev bf16 [E][N][K].
+ * expert_offsets_dev  int32 [E+1] as produced by w4a8_route_prep, offsets[E] <=
+ *                     R.  Offsets that do not start at 0, decrease or pass R
+ *                     make a call write nothing.
+ * C_bf16_dev          out bf16 [R][N], dA_bf16_dev out bf16 [R][K]: rows from
+ *                     offsets[E] on are left as they were.
+ * dW_dev, dW_type     out [E][N][K] of W4A8_TYPE_F32 or W4A8_TYPE_BF16; zeros
+ *                     for experts without rows.  accumulate != 0 adds the sum
+ *                     to what dW holds (in fp32, one rounding).
+ * Every run gives the same bits.  No output overlaps an input.
+ * Limits: 1 <= E <= W4A8_MAX_EXPERTS, R >= 0, 1 <= N <= W4A8_MAX_N, 1 <= K <=
+ * W4A8_MAX_K.  R == 0: nothing to do, except that wgrad writes its zeros.
+ * bf16 buffers need 2-byte, fp32 ones 4-byte alignment; with N % 8 == 0, K % 8
+ * == 0 and 16-byte alignment of all three the rows go to LDS as whole 16-byte
+ * pieces, otherwise through registers.
+ */
+int w4a8_grouped_gemm_bf16(const uint16_t* A_bf16_dev, const uint16_t* W_bf16_dev, const int32_t* expert_offsets_dev,
+                           int R, int E, int N, int K, uint16_t* C_bf16_dev, void* stream);
+int w4a8_grouped_gemm_dgrad(const uint16_t* dC_bf16_dev, const uint16_t* W_bf16_dev,
+                            const int32_t* expert_offsets_dev, int R, int E, int N, int K, uint16_t* dA_bf16_dev,
+                            void* stream);
+int w4a8_grouped_gemm_wgrad(const uint16_t* dC_bf16_dev, const uint16_t* A_bf16_dev,
+                            const int32_t* expert_offsets_dev, int R, int E, int N, int K, void* dW_dev, int dW_type,
+                            int accumulate, void* stream);
+
+/*
+ * w4a8_quantize_fp4 -- bf16 weights to the 4-bit formats of
+ * w4a8_grouped_gemm_a16 and w4a8_matvec (MXFP4 also of the other products):
+ *   W4A8_WSCALE_MX: per 32 K, scale 2^e with e = floor(log2 amax) - 2 (at least
+ *                   -127; 1 for a group of zeros), code = E2M1 of w / 2^e
+ *   W4A8_WSCALE_NV: gs[e] = amax of the expert / 2688 in fp32 (1 where amax < 2^-100),
+ *                   per 16 K s = E4M3FN of amax / (6 gs), code = E2M1 of w / (s gs)
+ * each to nearest, halves to the even code, past 6 to 6, decided on the exact
+ * quotient: the result is unique.  Signs of zeros are kept.  A group with an
+ * infinity or a NaN gets the NaN scale (0xFF, 0x7F) and codes 0; an expert's
+ * amax is of its finite values.
+ *
+ * w_bf16_dev         bf16 [E][N][K].  16-byte aligned.
+ * B_fp4_dev          out uint8 [E][N][K/2].  16-byte aligned.
+ * b_scales_dev       out uint8 [E][N][K/32] (MX) or [E][N][K/16] (NV).
+ * expert_scales_dev  out fp32 [E] with NV, NULL with MX.
+ * workspace_dev      w4a8_quantize_fp4_bytes(...) bytes (0 with MX: may be NULL),
+ *                    4-byte aligned, not shared by calls that may run at a time.
+ * Limits: 1 <= E <= W4A8_MAX_PREP_EXPERTS, 0 <= N <= W4A8_MAX_N, K % 32 == 0,
+ * 32 <= K <= W4A8_MAX_K.  N == 0 does nothing.
+ */
+int w4a8_quantize_fp4(const uint16_t* w_bf16_dev, int b_scale_format, int E, int N, int K, uint8_t* B_fp4_dev,
+                      uint8_t* b_scales_dev, float* expert_scales_dev, void* workspace_dev, size_t workspace_bytes,
+                      void* stream);
+
+/* Workspace of w4a8_quantize_fp4; 0 with MXFP4 and for sizes it refuses. */
+size_t w4a8_quantize_fp4_bytes(int b_scale_format, int E, int N, int K);
+
+/*
+ * w4a8_dequantize_fp4 -- its inverse: w[e, n, k] = bf16_rne(e2m1(code) * scale *
+ * gs[e]), in fp32 (exact before the bf16 rounding with MX and gs = 1).  NaN
+ * scale codes give NaN.  expert_scales_dev fp32 [E] or NULL for all ones;
+ * the rest as w4a8_quantize_fp4.
+ */
+int w4a8_dequantize_fp4(const uint8_t* B_fp4_dev, const uint8_t* b_scales_dev, int b_scale_format,
+                        const float* expert_scales_dev, int E, int N, int K, uint16_t* w_bf16_dev, void* stream);
+
+/*
+ * w4a8_quantize_gather_fp4 -- bf16 tokens to MXFP4 in the grouped row of every
+ * (token, slot): the input of w4a8_grouped_gemm_a4, quantised as MX weights
+ * are.
+ *
+ * x_bf16_dev       bf16 [T][K].  16-byte aligned.
+ * row_of_slot_dev  int32 [T*top_k] (as produced by w4a8_route_prep); slots
+ *                  whose row is outside [0, R) are skipped, no two others may
+ *                  name the same row.
+ * A_fp4_dev        out uint8 [R][K/2], 16-byte aligned, a_scales_dev out uint8
+ *                  [R][K/32] E8M0: rows that no slot names are left as they were.
+ * Limits: T >= 0, 1 <= top_k, T*top_k < 2^31, R >= 0, K % 32 == 0, 32 <= K <=
+ * W4A8_MAX_K.  T == 0 or R == 0 does nothing.
+ */
+int w4a8_quantize_gather_fp4(const uint16_t* x_bf16_dev, int T, int K, const int32_t* row_of_slot_dev, int top_k,
+                             int R, uint8_t* A_fp4_dev, uint8_t* a_scales_dev, void* stream);
+
+/*
+ * w4a8_grouped_gemm_a4 -- the grouped product of MXFP4 rows with MXFP4 weights:
+ *   C[r, n] = bf16_rne(sum over k of e2m1(A[r, k]) 2^(SA[r, k/32] - 127)
+ *                                   * e2m1(B[e, n, k]) 2^(SB[e, n, k/32] - 127))
+ * on the FP4 rate of the f8f6f4 matrix instruction, sums in fp32.
+ *
+ * A_fp4_dev           uint8 [R][K/2], a_scales_dev uint8 [R][K/32] E8M0.
+ * B_fp4_dev           uint8 [E][N][K/2], b_scales_dev uint8 [E][N][K/32] E8M0.
+ * expert_offsets_dev  as w4a8_grouped_gemm_bf16.
+ * C_bf16_dev          out bf16 [R][N]; rows from offsets[E] on are left as they were.
+ * A scale code of 0xFF makes its row or column of the product NaN.
+ * Limits: 1 <= E <= W4A8_MAX_EXPERTS, R >= 0, N % 32 == 0, 32 <= N <=
+ * W4A8_MAX_N, K % 128 == 0, 128 <= K <= W4A8_MAX_K.  R == 0 does nothing.
+ * A, B and C need 16-byte, the others 4-byte alignment.
+ */
+int w4a8_grouped_gemm_a4(const uint8_t* A_fp4_dev, const uint8_t* a_scales_dev, const uint8_t* B_fp4_dev,
+                         const uint8_t* b_scales_dev, const int32_t* expert_offsets_dev, int R, int E, int N, int K,
+                         uint16_t* C_bf16_dev, void* stream);
+
+/*
+ * w4a8_clip_grads -- the norm of n tensors as one vector and their scaling by it:
+ *   norm = sqrt(sum over all tensors of x^2),  c = min(1, max_norm / (norm + eps)),
+ *   out = c * x   (the product in fp32, rounded to the tensor's type)
+ * Squares and sums are in 64 bits.  A NaN or infinite gradient makes the norm
+ * NaN or infinite, and the outputs what the formula gives (NaN; 0 or NaN).
+ *
+ * tensors_host   n device pointers (a host array, read during the call, like
+ *                the three below).
+ * outs_host      n device pointers, or NULL: only the norm is taken.  outs[i] may be
+ *                tensors[i]; otherwise no output overlaps a tensor or another
+ *                output (W4A8_ERR_SHAPE).
+ * numel_host     int64 [n] elements; 0 is a tensor without any (its pointer may be NULL).
+ * types_host     int [n] W4A8_TYPE_F32 or W4A8_TYPE_BF16, of a tensor and its output.
+ * workspace_dev  w4a8_clip_grads_bytes(numel, n) bytes, 8-byte aligned, not
+ *                shared by calls that may run at a time.
+ * norm_dev       out fp32 [1].
+ * Every run gives the same bits.  Limits: 0 <= n <= 65536, numel >= 0, less
+ * than 2^44 elements in all, max_norm >= 0, eps >= 0.  Tensors need their
+ * type's alignment; where tensor and output are 16-byte aligned they move 16
+ * bytes at a time.  Uses host memory for a moment (W4A8_ERR_CAPACITY without).
+ */
+int w4a8_clip_grads(const void* const* tensors_host, void* const* outs_host, const int64_t* numel_host,
+                    const int* types_host, int n, float max_norm, float eps, void* workspace_dev,
+                    size_t workspace_bytes, float* norm_dev, void* stream);
+
+/* Workspace of w4a8_clip_grads; 0 for arguments it refuses. */
+size_t w4a8_clip_grads_bytes(const int64_t* numel_host, int n);
 
 /*
  * w4a8_plan_params -- the plan rule's constants, written to out_host[0..n-1]

@@ -28,6 +28,18 @@ torch when the caller does not pass them.
                                      -> y (bf16), few tokens; MXFP4, NVFP4 or INT4 (fmt 2) weights
     swiglu(C, checkpoint=False)      -> h (bf16), or h and an E4M3 copy of C (codes, scales)
     swiglu_backward(codes, scales, dh, dC=None, h=None) -> dC (and h) from that copy
+    rms_norm(x, weight, eps, residual=None) -> y (bf16), with residual (y, h = x + residual)
+    rms_norm_quant(x, weight, layout, eps, residual=None) -> A (E4M3 codes), SA (and h)
+    rms_norm_backward(h, weight, dy, eps, dh=None) -> dx, dweight
+    grouped_gemm_bf16(A, W, expert_offsets) -> C (bf16 weights)
+    grouped_gemm_dgrad(dC, W, expert_offsets) -> dA
+    grouped_gemm_wgrad(dC, A, expert_offsets, out=None, accumulate=False) -> dW
+    quantize_fp4(w, fmt)             -> B, SB, expert_scales (MXFP4 or NVFP4 weights of bf16 ones)
+    dequantize_fp4(B, SB, fmt, expert_scales=None) -> w (bf16)
+    quantize_gather_fp4(x, row_of_slot, top_k, R) -> A (MXFP4 codes), SA
+    grouped_gemm_a4(A, SA, B, SB, expert_offsets) -> C, MXFP4 rows and weights
+    grad_norm(tensors)               -> norm of them all
+    clip_grads(tensors, max_norm, eps, out=None) -> norm; the tensors scaled by min(1, max_norm / (norm + eps))
 """
 
 from ._lib import (  # noqa: F401
@@ -39,22 +51,34 @@ from ._lib import (  # noqa: F401
     WSCALE_MX,
     WSCALE_NV,
     W4A8Error,
+    clip_grads,
     combine,
     combine_backward,
+    dequantize_fp4,
     dispatch,
     dispatch_backward,
+    grad_norm,
     grouped_gemm,
     grouped_gemm_a16,
+    grouped_gemm_a4,
+    grouped_gemm_bf16,
+    grouped_gemm_dgrad,
     grouped_gemm_planned,
     grouped_gemm_planned_noalloc,
     grouped_gemm_swiglu,
+    grouped_gemm_wgrad,
     lib_path,
     load,
     matvec,
     plan,
     plan_bytes,
     plan_params,
+    quantize_fp4,
     quantize_gather,
+    quantize_gather_fp4,
+    rms_norm,
+    rms_norm_backward,
+    rms_norm_quant,
     route_prep,
     route_prep_waves,
     swiglu,

@@ -77,6 +77,31 @@ def _declare(lib):
     lib.w4a8_swiglu.restype = i32
     lib.w4a8_swiglu_backward.argtypes = [vp, vp, vp, i32, i32, vp, vp, vp]
     lib.w4a8_swiglu_backward.restype = i32
+    lib.w4a8_rms_norm.argtypes = [vp, vp, vp, i32, i32, i32, f32, vp, vp, vp, vp, i32, vp]
+    lib.w4a8_rms_norm.restype = i32
+    lib.w4a8_rms_norm_backward.argtypes = [vp, vp, i32, vp, vp, i32, i32, f32, vp, vp, vp, sz, vp]
+    lib.w4a8_rms_norm_backward.restype = i32
+    lib.w4a8_rms_norm_backward_bytes.argtypes = [i32, i32]
+    lib.w4a8_rms_norm_backward_bytes.restype = sz
+    for f in (lib.w4a8_grouped_gemm_bf16, lib.w4a8_grouped_gemm_dgrad):
+        f.argtypes = [vp, vp, vp, i32, i32, i32, i32, vp, vp]
+        f.restype = i32
+    lib.w4a8_grouped_gemm_wgrad.argtypes = [vp, vp, vp, i32, i32, i32, i32, vp, i32, i32, vp]
+    lib.w4a8_grouped_gemm_wgrad.restype = i32
+    lib.w4a8_quantize_fp4.argtypes = [vp, i32, i32, i32, i32, vp, vp, vp, vp, sz, vp]
+    lib.w4a8_quantize_fp4.restype = i32
+    lib.w4a8_quantize_fp4_bytes.argtypes = [i32, i32, i32, i32]
+    lib.w4a8_quantize_fp4_bytes.restype = sz
+    lib.w4a8_dequantize_fp4.argtypes = [vp, vp, i32, vp, i32, i32, i32, vp, vp]
+    lib.w4a8_dequantize_fp4.restype = i32
+    lib.w4a8_quantize_gather_fp4.argtypes = [vp, i32, i32, vp, i32, i32, vp, vp, vp]
+    lib.w4a8_quantize_gather_fp4.restype = i32
+    lib.w4a8_grouped_gemm_a4.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, vp, vp]
+    lib.w4a8_grouped_gemm_a4.restype = i32
+    lib.w4a8_clip_grads.argtypes = [vp, vp, vp, vp, i32, f32, f32, vp, sz, vp, vp]
+    lib.w4a8_clip_grads.restype = i32
+    lib.w4a8_clip_grads_bytes.argtypes = [vp, i32]
+    lib.w4a8_clip_grads_bytes.restype = sz
     lib.w4a8_plan_params.argtypes = [ctypes.POINTER(ctypes.c_int32), i32]
     lib.w4a8_plan_params.restype = i32
     lib.w4a8_status_string.argtypes = [i32]
@@ -663,3 +688,365 @@ def swiglu_backward(codes: torch.Tensor, scales: torch.Tensor, dh: torch.Tensor,
     _check("w4a8_swiglu_backward", lib.w4a8_swiglu_backward(_ptr(codes), _ptr(scales), _ptr(dh), R, I, _ptr(dC),
                                                             _ptr(h), _stream()))
     return dC if h is None else (dC, h)
+
+
+def _here(*tensors: Optional[torch.Tensor]):
+    """The tensors live on the current device, whose stream the call uses."""
+    dev = _current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"all tensors must be on the current device (cuda:{dev}), got {t.device}")
+
+
+def _weight_type(w: Optional[torch.Tensor], K: int, name: str = "weight") -> int:
+    if w is None:
+        return 0
+    if isinstance(w, _Tensor) and w.dtype not in (torch.float32, _bfloat16):
+        raise TypeError(f"{name} must be float32 or bfloat16, got {w.dtype}")
+    _need(w, name, getattr(w, "dtype", None), K)
+    return 0 if w.dtype is torch.float32 else 1
+
+
+def _rms_norm(x, weight, eps, residual, y, sum_out, A, SA, layout):
+    T, K = x.shape
+    kind = _weight_type(weight, K)
+    _here(x, weight, residual, y, sum_out, A, SA)
+    _check("w4a8_rms_norm", load().w4a8_rms_norm(
+        _ptr(x), _ptr(residual), _ptr(weight), kind, T, K, float(eps), _ptr(y), _ptr(sum_out), _ptr(A), _ptr(SA),
+        int(layout), _stream()))
+
+
+def _norm_inputs(x, residual, sum_out):
+    if x.dim() != 2:
+        raise ValueError("x must be [T, K]")
+    _bf16(x, "x")
+    if residual is None:
+        if sum_out is not None:
+            raise ValueError("sum_out goes with a residual")
+        return None
+    _bf16(residual, "residual", x.numel())
+    if sum_out is None:
+        sum_out = torch.empty(x.shape, dtype=_bfloat16, device=x.device)
+    _bf16(sum_out, "sum_out", x.numel())
+    return sum_out
+
+
+def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+             residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+             sum_out: Optional[torch.Tensor] = None):
+    """y bf16 [T, K] = h / sqrt(mean(h^2) + eps) * weight of x bf16 [T, K]; with
+    residual bf16 [T, K], (y, h) with h = bf16(x + residual), otherwise h = x.
+    weight fp32 or bf16 [K], or None for ones.  out and sum_out may be x or
+    residual."""
+    load()
+    sum_out = _norm_inputs(x, residual, sum_out)
+    if out is None:
+        out = torch.empty(x.shape, dtype=_bfloat16, device=x.device)
+    _bf16(out, "out", x.numel())
+    _rms_norm(x, weight, eps, residual, out, sum_out, None, None, 0)
+    return out if residual is None else (out, sum_out)
+
+
+def rms_norm_quant(x: torch.Tensor, weight: Optional[torch.Tensor], layout: int, eps: float = 1e-6,
+                   residual: Optional[torch.Tensor] = None, A: Optional[torch.Tensor] = None,
+                   SA: Optional[torch.Tensor] = None, sum_out: Optional[torch.Tensor] = None,
+                   out: Optional[torch.Tensor] = None):
+    """The same norm in 8 bits, the input of grouped_gemm: (A uint8 [T, K] E4M3
+    codes, SA fp32 [T, K/128] for layout 0 or [K/128, T] for layout 1), with
+    residual (A, SA, h).  out bf16 [T, K], where given, gets y too."""
+    load()
+    sum_out = _norm_inputs(x, residual, sum_out)
+    T, K = x.shape
+    if K % 128:
+        raise ValueError("K must be a multiple of 128")
+    if A is None:
+        A = torch.empty((T, K), dtype=torch.uint8, device=x.device)
+    if SA is None:
+        SA = torch.empty((T, K // 128) if layout == 0 else (K // 128, T), dtype=torch.float32, device=x.device)
+    _need(A, "A", torch.uint8, T * K)
+    _need(SA, "a_scales", torch.float32, T * (K // 128))
+    if out is not None:
+        _bf16(out, "out", T * K)
+    _rms_norm(x, weight, eps, residual, out, sum_out, A, SA, layout)
+    return (A, SA) if residual is None else (A, SA, sum_out)
+
+
+def rms_norm_backward(h: torch.Tensor, weight: Optional[torch.Tensor], dy: torch.Tensor, eps: float = 1e-6,
+                      dh: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
+                      dweight: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """(dx bf16 [T, K], dweight fp32 [K]) of rms_norm from h, its sum (its x
+    without a residual), and dy bf16 [T, K]; dh bf16 [T, K], the gradient that
+    reaches h beside y, is added.  dx is the gradient of x and of residual; it
+    may be the buffer of dy, dh or h."""
+    lib = load()
+    if h.dim() != 2:
+        raise ValueError("h must be [T, K]")
+    T, K = h.shape
+    _bf16(h, "h")
+    kind = _weight_type(weight, K)
+    _bf16(dy, "dy", T * K)
+    if dh is not None:
+        _bf16(dh, "dh", T * K)
+    if dx is None:
+        dx = torch.empty((T, K), dtype=_bfloat16, device=h.device)
+    if dweight is None:
+        dweight = torch.empty(K, dtype=torch.float32, device=h.device)
+    _bf16(dx, "dx", T * K)
+    _need(dweight, "dweight", torch.float32, K)
+    need = lib.w4a8_rms_norm_backward_bytes(T, K)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=h.device)
+    _need(workspace, "workspace", torch.uint8)
+    _here(h, weight, dy, dh, dx, dweight, workspace)
+    _check("w4a8_rms_norm_backward", lib.w4a8_rms_norm_backward(
+        _ptr(h), _ptr(weight), kind, _ptr(dy), _ptr(dh), T, K, float(eps), _ptr(dx), _ptr(dweight), _ptr(workspace),
+        workspace.numel(), _stream()))
+    return dx, dweight
+
+
+def _product(rows: torch.Tensor, W: torch.Tensor, expert_offsets: torch.Tensor, axis: int):
+    """Shapes of a product of rows with bf16 weights; axis: of W that the rows have."""
+    if rows.dim() != 2 or W.dim() != 3:
+        raise ValueError("rows must be two-dimensional, W [E, N, K]")
+    if rows.shape[1] != W.shape[axis]:
+        raise ValueError("inconsistent shapes of the rows and W")
+    _need(expert_offsets, "expert_offsets", torch.int32, W.shape[0] + 1)
+    return rows.shape[0], *W.shape
+
+
+def grouped_gemm_bf16(A: torch.Tensor, W: torch.Tensor, expert_offsets: torch.Tensor,
+                      out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """C bf16 [R, N] of the grouped product with bf16 weights: A bf16 [R, K], W
+    bf16 [E, N, K], expert_offsets int32 [E+1].  Rows from offsets[E] on are
+    left as `out` holds them, undefined where it is not given."""
+    lib = load()
+    _bf16(A, "A")
+    _bf16(W, "W")
+    R, E, N, K = _product(A, W, expert_offsets, 2)
+    if out is None:
+        out = torch.empty((R, N), dtype=_bfloat16, device=A.device)
+    _bf16(out, "out", R * N)
+    _here(A, W, expert_offsets, out)
+    _check("w4a8_grouped_gemm_bf16", lib.w4a8_grouped_gemm_bf16(
+        _ptr(A), _ptr(W), _ptr(expert_offsets), R, E, N, K, _ptr(out), _stream()))
+    return out
+
+
+def grouped_gemm_dgrad(dC: torch.Tensor, W: torch.Tensor, expert_offsets: torch.Tensor,
+                       out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """dA bf16 [R, K] of grouped_gemm_bf16 from dC bf16 [R, N] and its W."""
+    lib = load()
+    _bf16(dC, "dC")
+    _bf16(W, "W")
+    R, E, N, K = _product(dC, W, expert_offsets, 1)
+    if out is None:
+        out = torch.empty((R, K), dtype=_bfloat16, device=dC.device)
+    _bf16(out, "out", R * K)
+    _here(dC, W, expert_offsets, out)
+    _check("w4a8_grouped_gemm_dgrad", lib.w4a8_grouped_gemm_dgrad(
+        _ptr(dC), _ptr(W), _ptr(expert_offsets), R, E, N, K, _ptr(out), _stream()))
+    return out
+
+
+def grouped_gemm_wgrad(dC: torch.Tensor, A: torch.Tensor, expert_offsets: torch.Tensor,
+                       out: Optional[torch.Tensor] = None, accumulate: bool = False) -> torch.Tensor:
+    """dW [E, N, K] of grouped_gemm_bf16 from dC bf16 [R, N] and its A bf16 [R,
+    K]: fp32, or the type of `out` (fp32 or bf16); with accumulate added to what
+    `out` holds.  Experts without rows have zeros (nothing added)."""
+    lib = load()
+    _bf16(dC, "dC")
+    _bf16(A, "A")
+    if dC.dim() != 2 or A.dim() != 2 or dC.shape[0] != A.shape[0]:
+        raise ValueError("dC must be [R, N], A [R, K]")
+    R, N = dC.shape
+    K = A.shape[1]
+    E = expert_offsets.numel() - 1
+    _need(expert_offsets, "expert_offsets", torch.int32)
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate adds to a given out")
+        out = torch.empty((E, N, K), dtype=torch.float32, device=dC.device)
+    if out.dtype is torch.float32:
+        _need(out, "out", torch.float32, E * N * K)
+    else:
+        _bf16(out, "out", E * N * K)
+    _here(dC, A, expert_offsets, out)
+    _check("w4a8_grouped_gemm_wgrad", lib.w4a8_grouped_gemm_wgrad(
+        _ptr(dC), _ptr(A), _ptr(expert_offsets), R, E, N, K, _ptr(out), 0 if out.dtype is torch.float32 else 1,
+        int(accumulate), _stream()))
+    return out
+
+
+def _fp4_shape(t: torch.Tensor, name: str):
+    if t.dim() not in (2, 3):
+        raise ValueError(f"{name} must be [N, K] or [E, N, K] (K/2 codes)")
+    return (1, *t.shape) if t.dim() == 2 else tuple(t.shape)
+
+
+def quantize_fp4(w: torch.Tensor, fmt: int, B: Optional[torch.Tensor] = None, SB: Optional[torch.Tensor] = None,
+                 expert_scales: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """bf16 weights [E, N, K] (or [N, K], one expert) -> (B uint8 [.., K/2] packed
+    E2M1, SB uint8 [.., K/32] E8M0 for fmt WSCALE_MX or [.., K/16] E4M3 for
+    WSCALE_NV, expert_scales fp32 [E] for WSCALE_NV, None for WSCALE_MX), as
+    grouped_gemm_a16 and matvec take them (MXFP4 also the other products)."""
+    lib = load()
+    E, N, K = _fp4_shape(w, "w")
+    _bf16(w, "w")
+    if fmt not in (WSCALE_MX, WSCALE_NV):
+        raise ValueError("fmt must be WSCALE_MX or WSCALE_NV")
+    if K < 32 or K % 32:
+        raise ValueError("K must be a multiple of 32")
+    block = 32 if fmt == WSCALE_MX else 16
+    if fmt == WSCALE_MX and expert_scales is not None:
+        raise ValueError("expert_scales go with WSCALE_NV")
+    lead = tuple(w.shape[:-1])
+    if B is None:
+        B = torch.empty((*lead, K // 2), dtype=torch.uint8, device=w.device)
+    if SB is None:
+        SB = torch.empty((*lead, K // block), dtype=torch.uint8, device=w.device)
+    if fmt == WSCALE_NV and expert_scales is None:
+        expert_scales = torch.empty(E, dtype=torch.float32, device=w.device)
+    _need(B, "B", torch.uint8, E * N * (K // 2))
+    _need(SB, "b_scales", torch.uint8, E * N * (K // block))
+    if expert_scales is not None:
+        _need(expert_scales, "expert_scales", torch.float32, E)
+    need = lib.w4a8_quantize_fp4_bytes(int(fmt), E, N, K)
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=w.device)
+    if workspace is not None:
+        _need(workspace, "workspace", torch.uint8)
+    _here(w, B, SB, expert_scales, workspace)
+    if E * N:
+        _check("w4a8_quantize_fp4", lib.w4a8_quantize_fp4(
+            _ptr(w), int(fmt), E, N, K, _ptr(B), _ptr(SB), _ptr(expert_scales), _ptr(workspace),
+            0 if workspace is None else workspace.numel(), _stream()))
+    return B, SB, expert_scales
+
+
+def dequantize_fp4(B: torch.Tensor, SB: torch.Tensor, fmt: int, expert_scales: Optional[torch.Tensor] = None,
+                   out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """bf16 weights [.., K] of packed 4-bit ones: B uint8 [E, N, K/2] or [N, K/2],
+    SB and expert_scales (fp32 [E] or None for ones) as quantize_fp4 gives them."""
+    lib = load()
+    E, N, Kh = _fp4_shape(B, "B")
+    K = 2 * Kh
+    _need(B, "B", torch.uint8)
+    if fmt not in (WSCALE_MX, WSCALE_NV):
+        raise ValueError("fmt must be WSCALE_MX or WSCALE_NV")
+    if K < 32 or K % 32:
+        raise ValueError("K must be a multiple of 32")
+    _need(SB, "b_scales", torch.uint8, E * N * (K // (32 if fmt == WSCALE_MX else 16)))
+    if expert_scales is not None:
+        _need(expert_scales, "expert_scales", torch.float32, E)
+    if out is None:
+        out = torch.empty((*B.shape[:-1], K), dtype=_bfloat16, device=B.device)
+    _bf16(out, "out", E * N * K)
+    _here(B, SB, expert_scales, out)
+    if E * N:
+        _check("w4a8_dequantize_fp4", lib.w4a8_dequantize_fp4(
+            _ptr(B), _ptr(SB), int(fmt), _ptr(expert_scales), E, N, K, _ptr(out), _stream()))
+    return out
+
+
+def quantize_gather_fp4(x: torch.Tensor, row_of_slot: torch.Tensor, top_k: int, R: int,
+                        A: Optional[torch.Tensor] = None, SA: Optional[torch.Tensor] = None):
+    """bf16 tokens x [T, K] -> (A uint8 [R, K/2] packed E2M1, SA uint8 [R, K/32]
+    E8M0) in the grouped row of every slot (row_of_slot int32 [T * top_k]); rows
+    without a slot keep what A and SA hold, zeros where they are not given."""
+    lib = load()
+    if x.dim() != 2:
+        raise ValueError("x must be [T, K]")
+    T, K = x.shape
+    _bf16(x, "x")
+    if K < 32 or K % 32:
+        raise ValueError("K must be a multiple of 32")
+    _need(row_of_slot, "row_of_slot", torch.int32, T * top_k)
+    if A is None:
+        A = torch.zeros((R, K // 2), dtype=torch.uint8, device=x.device)
+    if SA is None:
+        SA = torch.zeros((R, K // 32), dtype=torch.uint8, device=x.device)
+    _need(A, "A", torch.uint8, R * (K // 2))
+    _need(SA, "a_scales", torch.uint8, R * (K // 32))
+    _here(x, row_of_slot, A, SA)
+    _check("w4a8_quantize_gather_fp4", lib.w4a8_quantize_gather_fp4(
+        _ptr(x), T, K, _ptr(row_of_slot), int(top_k), int(R), _ptr(A), _ptr(SA), _stream()))
+    return A, SA
+
+
+def grouped_gemm_a4(A: torch.Tensor, SA: torch.Tensor, B: torch.Tensor, SB: torch.Tensor,
+                    expert_offsets: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """C bf16 [R, N] of the grouped product of MXFP4 rows and weights: A uint8
+    [R, K/2], SA uint8 [R, K/32], B uint8 [E, N, K/2], SB uint8 [E, N, K/32],
+    expert_offsets int32 [E+1].  Rows from offsets[E] on are left as `out` holds
+    them, undefined where it is not given."""
+    lib = load()
+    if A.dim() != 2 or B.dim() != 3 or SB.dim() != 3:
+        raise ValueError("A must be [R, K/2], B [E, N, K/2], SB [E, N, K/32]")
+    R, Kh = A.shape
+    E, N, K = B.shape[0], B.shape[1], 2 * B.shape[2]
+    if 2 * Kh != K or SB.shape != (E, N, K // 32):
+        raise ValueError("inconsistent K between A, B and SB")
+    _need(A, "A", torch.uint8)
+    _need(SA, "a_scales", torch.uint8, R * (K // 32))
+    _need(B, "B", torch.uint8)
+    _need(SB, "b_scales", torch.uint8)
+    _need(expert_offsets, "expert_offsets", torch.int32, E + 1)
+    if out is None:
+        out = torch.empty((R, N), dtype=_bfloat16, device=A.device)
+    _bf16(out, "out", R * N)
+    _here(A, SA, B, SB, expert_offsets, out)
+    _check("w4a8_grouped_gemm_a4", lib.w4a8_grouped_gemm_a4(
+        _ptr(A), _ptr(SA), _ptr(B), _ptr(SB), _ptr(expert_offsets), R, E, N, K, _ptr(out), _stream()))
+    return out
+
+
+def _grads(tensors, outs, max_norm, eps, norm, workspace):
+    lib = load()
+    tensors = list(tensors)
+    n = len(tensors)
+    types = (ctypes.c_int * n)()
+    numel = (ctypes.c_int64 * n)()
+    for i, t in enumerate(tensors):
+        if isinstance(t, _Tensor) and t.dtype not in (torch.float32, _bfloat16):
+            raise TypeError(f"tensor {i} must be float32 or bfloat16, got {t.dtype}")
+        _need(t, f"tensor {i}", getattr(t, "dtype", None))
+        types[i] = 0 if t.dtype is torch.float32 else 1
+        numel[i] = t.numel()
+    if outs is not None:
+        outs = list(outs)
+        if len(outs) != n:
+            raise ValueError(f"out must hold {n} tensors, got {len(outs)}")
+        for i, (t, o) in enumerate(zip(tensors, outs)):
+            _need(o, f"out {i}", t.dtype, t.numel())
+        _here(*outs)
+    _here(*tensors)
+    if norm is None:
+        norm = torch.empty(1, dtype=torch.float32, device=torch.device("cuda", _current_device()))
+    _need(norm, "norm", torch.float32, 1)
+    need = lib.w4a8_clip_grads_bytes(numel, n)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=norm.device)
+    _need(workspace, "workspace", torch.uint8)
+    _here(norm, workspace)
+    ptrs = (ctypes.c_void_p * n)(*[t.data_ptr() for t in tensors])
+    optrs = None if outs is None else (ctypes.c_void_p * n)(*[t.data_ptr() for t in outs])
+    _check("w4a8_clip_grads", lib.w4a8_clip_grads(
+        ptrs, optrs, numel, types, n, float(max_norm), float(eps), _ptr(workspace), workspace.numel(), _ptr(norm),
+        _stream()))
+    return norm
+
+
+def grad_norm(tensors, norm: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """norm fp32 [1] = sqrt of the sum of all squares of a list of contiguous fp32
+    and bf16 tensors, summed in 64 bits."""
+    return _grads(tensors, None, 0.0, 0.0, norm, workspace)
+
+
+def clip_grads(tensors, max_norm: float, eps: float = 1e-6, out=None, norm: Optional[torch.Tensor] = None,
+               workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Scale a list of contiguous fp32 and bf16 tensors by min(1, max_norm /
+    (norm + eps)), norm that of them all (grad_norm), and return the norm, fp32
+    [1].  In place, or into the tensors of the list `out`; no tensor may be in
+    the list twice."""
+    tensors = list(tensors)
+    return _grads(tensors, tensors if out is None else out, max_norm, eps, norm, workspace)

@@ -20,7 +20,8 @@ CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libw4a8.so")
 SOURCES = ["api.cpp", "prep.hip", "gemm.hip", "quant.hip", "combine.hip", "a16.hip",
-           "gate.hip", "dispatch.hip", "matvec.hip", "swiglu_train.hip"]
+           "gate.hip", "dispatch.hip", "matvec.hip", "swiglu_train.hip",
+           "rms_norm.hip", "grad_norm.hip", "fp4.hip", "tile_gemm.hip"]
 # roofline probes (sustained MFMA rate and HBM read bandwidth), a library of
 # their own: the benchmark loads them, the GEMM path does not
 PROBE_LIB = os.path.join(HERE, "libw4a8_probe.so")
@@ -56,7 +57,7 @@ def compile_flags(debug: bool = False):
 # sources that issue inline-asm memory operations: their device assembly is
 # checked after every build (see asmcheck.py); with the rule for loads to LDS
 # where a kernel waits for all of them before it reads any
-ASM_CHECKED = {"gemm.hip": False, "matvec.hip": True}
+ASM_CHECKED = {"gemm.hip": False, "matvec.hip": True, "tile_gemm.hip": False}
 
 
 def check_device_asm(cc: str, tmp: str, verbose: bool = False) -> None:

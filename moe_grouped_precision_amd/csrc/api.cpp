@@ -9,6 +9,7 @@
 #include <algorithm>
 #include <cstring>
 #include <mutex>
+#include <vector>
 
 #include "w4a8_device.h"
 #include "w4a8_launch.h"
@@ -113,6 +114,75 @@ int check_gemm_shape(int E, int N, int K, int max_experts = W4A8_MAX_EXPERTS) {
     return fail(W4A8_ERR_SHAPE, "K=%d must be a multiple of 128 in [128, %d]", K, W4A8_MAX_K);
   if (N < 32 || N % 32 || N > W4A8_MAX_N)
     return fail(W4A8_ERR_SHAPE, "N=%d must be a multiple of 32 in [32, %d]", N, W4A8_MAX_N);
+  return W4A8_OK;
+}
+
+int check_norm(int T, int K, float eps, const void* weight, int weight_type) {
+  if (T < 0 || K < 1 || K > W4A8_MAX_K) return fail(W4A8_ERR_SHAPE, "T=%d, K=%d outside [1, %d]", T, K, W4A8_MAX_K);
+  if (!(eps >= 0.0f)) return fail(W4A8_ERR_SHAPE, "eps must not be negative or NaN");
+  if (weight_type != W4A8_TYPE_F32 && weight_type != W4A8_TYPE_BF16)
+    return fail(W4A8_ERR_LAYOUT, "weight_type=%d is neither fp32 (0) nor bf16 (1)", weight_type);
+  if (!aligned(weight, weight_type == W4A8_TYPE_F32 ? 4 : 2))
+    return fail(W4A8_ERR_ALIGN, "the weight needs the alignment of its type");
+  return W4A8_OK;
+}
+
+int check_bf16_product(int R, int E, int N, int K) {
+  if (R < 0 || E < 1 || E > W4A8_MAX_EXPERTS)
+    return fail(W4A8_ERR_SHAPE, "R=%d, E=%d outside [1, %d]", R, E, W4A8_MAX_EXPERTS);
+  if (N < 1 || N > W4A8_MAX_N || K < 1 || K > W4A8_MAX_K)
+    return fail(W4A8_ERR_SHAPE, "N=%d outside [1, %d] or K=%d outside [1, %d]", N, W4A8_MAX_N, K, W4A8_MAX_K);
+  return W4A8_OK;
+}
+
+w4a8::TileArgs bf16_product(const uint16_t* Y, const uint16_t* X, const int32_t* offsets, void* out, int E, int R,
+                            int N, int K, int accumulate) {
+  return {reinterpret_cast<const uint8_t*>(Y), reinterpret_cast<const uint8_t*>(X), nullptr, nullptr, offsets, out,
+          E, R, N, K, accumulate};
+}
+
+int check_fp4(int fmt, int E, int N, int K) {
+  if (fmt != W4A8_WSCALE_MX && fmt != W4A8_WSCALE_NV)
+    return fail(W4A8_ERR_LAYOUT, "b_scale_format=%d is neither MXFP4 (0) nor NVFP4 (1)", fmt);
+  if (E < 1 || E > W4A8_MAX_PREP_EXPERTS || N < 0 || N > W4A8_MAX_N)
+    return fail(W4A8_ERR_SHAPE, "E=%d outside [1, %d] or N=%d outside [0, %d]", E, W4A8_MAX_PREP_EXPERTS, N,
+                W4A8_MAX_N);
+  if (K < 32 || K % 32 || K > W4A8_MAX_K)
+    return fail(W4A8_ERR_SHAPE, "K=%d must be a multiple of 32 in [32, %d]", K, W4A8_MAX_K);
+  return W4A8_OK;
+}
+
+constexpr int kMaxGrads = 65536;
+constexpr int64_t kMaxGradElements = (int64_t)1 << 44;
+
+// No output of a list may overlap another output or a tensor other than its
+// own: such elements would be scaled twice, or read after they were scaled.
+int check_outputs_apart(const void* const* in, void* const* out, const int64_t* numel, const int* types, int n) {
+  struct Range {
+    uintptr_t lo, hi;
+    bool out;
+  };
+  try {
+    std::vector<Range> all;
+    all.reserve(2 * (size_t)n);
+    for (int i = 0; i < n; ++i) {
+      if (numel[i] == 0) continue;
+      const uintptr_t bytes = (uintptr_t)numel[i] * (types[i] == W4A8_TYPE_F32 ? 4 : 2);
+      const uintptr_t a = reinterpret_cast<uintptr_t>(in[i]), b = reinterpret_cast<uintptr_t>(out[i]);
+      all.push_back({b, b + bytes, true});
+      if (a != b) all.push_back({a, a + bytes, false});
+    }
+    std::sort(all.begin(), all.end(), [](const Range& x, const Range& y) { return x.lo < y.lo; });
+    uintptr_t any_end = 0, out_end = 0;
+    for (const Range& r : all) {
+      if (r.lo < (r.out ? any_end : out_end))
+        return fail(W4A8_ERR_SHAPE, "an output overlaps another output or another tensor");
+      any_end = std::max(any_end, r.hi);
+      if (r.out) out_end = std::max(out_end, r.hi);
+    }
+  } catch (...) {
+    return fail(W4A8_ERR_CAPACITY, "no host memory to check %d outputs", n);
+  }
   return W4A8_OK;
 }
 
@@ -582,6 +652,256 @@ int w4a8_swiglu_backward(const uint8_t* ckpt_fp8_dev, const float* ckpt_scales_d
   hipError_t e = w4a8::launch_swiglu_backward(ckpt_fp8_dev, ckpt_scales_dev, dh_bf16_dev, R, I, dC_bf16_dev,
                                               h_bf16_dev, (hipStream_t)stream);
   if (e != hipSuccess) return fail(W4A8_ERR_HIP, "swiglu_backward launch: %s", hipGetErrorString(e));
+  return ok();
+}
+
+size_t w4a8_rms_norm_backward_bytes(int T, int K) {
+  if (T < 1 || K < 1 || K > W4A8_MAX_K) return 0;
+  return (size_t)w4a8::norm_backward_parts(T) * K * sizeof(float);
+}
+
+int w4a8_rms_norm(const uint16_t* x_bf16_dev, const uint16_t* residual_bf16_dev, const void* weight_dev,
+                  int weight_type, int T, int K, float eps, uint16_t* y_bf16_dev, uint16_t* sum_bf16_dev,
+                  uint8_t* A_fp8_dev, float* a_scales_dev, int a_scale_layout, void* stream) {
+  int st = check_norm(T, K, eps, weight_dev, weight_type);
+  if (st != W4A8_OK) return st;
+  if (A_fp8_dev && K % 128) return fail(W4A8_ERR_SHAPE, "K=%d must be a multiple of 128 with 8-bit output", K);
+  if (a_scale_layout != W4A8_SCALE_ROW_MAJOR && a_scale_layout != W4A8_SCALE_M_MAJOR)
+    return fail(W4A8_ERR_LAYOUT, "a_scale_layout=%d is neither row-major (0) nor M-major (1)", a_scale_layout);
+  if (!A_fp8_dev != !a_scales_dev) return fail(W4A8_ERR_NULL, "8-bit codes and scales go together");
+  if (T > 0 && (!x_bf16_dev || (!y_bf16_dev && !A_fp8_dev))) return fail(W4A8_ERR_NULL, "null pointer argument");
+  if (!aligned(x_bf16_dev, 2) || !aligned(residual_bf16_dev, 2) || !aligned(y_bf16_dev, 2) ||
+      !aligned(sum_bf16_dev, 2) || !aligned(A_fp8_dev, 16) || !aligned(a_scales_dev, 4))
+    return fail(W4A8_ERR_ALIGN, "x, residual, y and sum need 2-byte, A 16-byte, scales 4-byte alignment");
+  const DeviceInfo* d = nullptr;
+  st = device_info(&d);
+  if (st != W4A8_OK) return st;
+  if (T == 0) return ok();
+  const w4a8::NormArgs args{x_bf16_dev, residual_bf16_dev, weight_dev, y_bf16_dev, sum_bf16_dev, A_fp8_dev,
+                            a_scales_dev, T, K, weight_type == W4A8_TYPE_F32, a_scale_layout, eps};
+  hipError_t e = w4a8::launch_rms_norm(args, (hipStream_t)stream);
+  if (e != hipSuccess) return fail(W4A8_ERR_HIP, "rms_norm launch: %s", hipGetErrorString(e));
+  return ok();
+}
+
+int w4a8_rms_norm_backward(const uint16_t* h_bf16_dev, const void* weight_dev, int weight_type,
+                           const uint16_t* dy_bf16_dev, const uint16_t* dsum_bf16_dev, int T, int K, float eps,
+                           uint16_t* dx_bf16_dev, float* dweight_dev, void* workspace_dev, size_t workspace_bytes,
+                           void* stream) {
+  int st = check_norm(T, K, eps, weight_dev, weight_type);
+  if (st != W4A8_OK) return st;
+  if (T > 0 && (!h_bf16_dev || !dy_bf16_dev || !dx_bf16_dev || !workspace_dev))
+    return fail(W4A8_ERR_NULL, "null pointer argument");
+  if (!aligned(h_bf16_dev, 2) || !aligned(dy_bf16_dev, 2) || !aligned(dsum_bf16_dev, 2) || !aligned(dx_bf16_dev, 2) ||
+      !aligned(dweight_dev, 4) || !aligned(workspace_dev, 4))
+    return fail(W4A8_ERR_ALIGN, "h, dy, dsum and dx need 2-byte, dweight and workspace 4-byte alignment");
+  if (workspace_bytes < w4a8_rms_norm_backward_bytes(T, K))
+    return fail(W4A8_ERR_CAPACITY, "workspace of %zu bytes, %zu needed", workspace_bytes,
+                w4a8_rms_norm_backward_bytes(T, K));
+  const DeviceInfo* d = nullptr;
+  st = device_info(&d);
+  if (st != W4A8_OK) return st;
+  const w4a8::NormGradArgs args{h_bf16_dev, dy_bf16_dev, dsum_bf16_dev, weight_dev, dx_bf16_dev, dweight_dev,
+                                static_cast<float*>(workspace_dev), T, K, weight_type == W4A8_TYPE_F32, eps};
+  hipError_t e = w4a8::launch_rms_norm_backward(args, (hipStream_t)stream);
+  if (e != hipSuccess) return fail(W4A8_ERR_HIP, "rms_norm_backward launch: %s", hipGetErrorString(e));
+  return ok();
+}
+
+int w4a8_grouped_gemm_bf16(const uint16_t* A_bf16_dev, const uint16_t* W_bf16_dev, const int32_t* expert_offsets_dev,
+                           int R, int E, int N, int K, uint16_t* C_bf16_dev, void* stream) {
+  int st = check_bf16_product(R, E, N, K);
+  if (st != W4A8_OK) return st;
+  if (R > 0 && (!A_bf16_dev || !W_bf16_dev || !expert_offsets_dev || !C_bf16_dev))
+    return fail(W4A8_ERR_NULL, "null pointer argument");
+  if (!aligned(A_bf16_dev, 2) || !aligned(W_bf16_dev, 2) || !aligned(C_bf16_dev, 2) || !aligned(expert_offsets_dev, 4))
+    return fail(W4A8_ERR_ALIGN, "A, W and C need 2-byte, offsets 4-byte alignment");
+  const DeviceInfo* d = nullptr;
+  st = device_info(&d);
+  if (st != W4A8_OK) return st;
+  if (R == 0) return ok();
+  hipError_t e = w4a8::launch_grouped_bf16(bf16_product(A_bf16_dev, W_bf16_dev, expert_offsets_dev, C_bf16_dev, E, R,
+                                                        N, K, 0), (hipStream_t)stream);
+  if (e != hipSuccess) return fail(W4A8_ERR_HIP, "grouped_gemm_bf16 launch: %s", hipGetErrorString(e));
+  return ok();
+}
+
+int w4a8_grouped_gemm_dgrad(const uint16_t* dC_bf16_dev, const uint16_t* W_bf16_dev,
+                            const int32_t* expert_offsets_dev, int R, int E, int N, int K, uint16_t* dA_bf16_dev,
+                            void* stream) {
+  int st = check_bf16_product(R, E, N, K);
+  if (st != W4A8_OK) return st;
+  if (R > 0 && (!dC_bf16_dev || !W_bf16_dev || !expert_offsets_dev || !dA_bf16_dev))
+    return fail(W4A8_ERR_NULL, "null pointer argument");
+  if (!aligned(dC_bf16_dev, 2) || !aligned(W_bf16_dev, 2) || !aligned(dA_bf16_dev, 2) ||
+      !aligned(expert_offsets_dev, 4))
+    return fail(W4A8_ERR_ALIGN, "dC, W and dA need 2-byte, offsets 4-byte alignment");
+  const DeviceInfo* d = nullptr;
+  st = device_info(&d);
+  if (st != W4A8_OK) return st;
+  if (R == 0) return ok();
+  hipError_t e = w4a8::launch_grouped_dgrad(bf16_product(dC_bf16_dev, W_bf16_dev, expert_offsets_dev, dA_bf16_dev, E,
+                                                         R, N, K, 0), (hipStream_t)stream);
+  if (e != hipSuccess) return fail(W4A8_ERR_HIP, "grouped_gemm_dgrad launch: %s", hipGetErrorString(e));
+  return ok();
+}
+
+int w4a8_grouped_gemm_wgrad(const uint16_t* dC_bf16_dev, const uint16_t* A_bf16_dev,
+                            const int32_t* expert_offsets_dev, int R, int E, int N, int K, void* dW_dev, int dW_type,
+                            int accumulate, void* stream) {
+  int st = check_bf16_product(R, E, N, K);
+  if (st != W4A8_OK) return st;
+  if (dW_type != W4A8_TYPE_F32 && dW_type != W4A8_TYPE_BF16)
+    return fail(W4A8_ERR_LAYOUT, "dW_type=%d is neither fp32 (0) nor bf16 (1)", dW_type);
+  if (!dW_dev || !expert_offsets_dev || (R > 0 && (!dC_bf16_dev || !A_bf16_dev)))
+    return fail(W4A8_ERR_NULL, "null pointer argument");
+  if (!aligned(dC_bf16_dev, 2) || !aligned(A_bf16_dev, 2) || !aligned(dW_dev, dW_type == W4A8_TYPE_F32 ? 4 : 2) ||
+      !aligned(expert_offsets_dev, 4))
+    return fail(W4A8_ERR_ALIGN, "dC and A need 2-byte, dW its type's, offsets 4-byte alignment");
+  const DeviceInfo* d = nullptr;
+  st = device_info(&d);
+  if (st != W4A8_OK) return st;
+  hipError_t e = w4a8::launch_grouped_wgrad(bf16_product(dC_bf16_dev, A_bf16_dev, expert_offsets_dev, dW_dev, E, R, N,
+                                                         K, accumulate != 0),
+                                            dW_type == W4A8_TYPE_F32, (hipStream_t)stream);
+  if (e != hipSuccess) return fail(W4A8_ERR_HIP, "grouped_gemm_wgrad launch: %s", hipGetErrorString(e));
+  return ok();
+}
+
+size_t w4a8_quantize_fp4_bytes(int b_scale_format, int E, int N, int K) {
+  if (b_scale_format != W4A8_WSCALE_NV || E < 1 || E > W4A8_MAX_PREP_EXPERTS || N < 1 || N > W4A8_MAX_N || K < 32 ||
+      K % 32 || K > W4A8_MAX_K)
+    return 0;
+  return w4a8::quant_fp4_workspace(true, E, N, K);
+}
+
+int w4a8_quantize_fp4(const uint16_t* w_bf16_dev, int b_scale_format, int E, int N, int K, uint8_t* B_fp4_dev,
+                      uint8_t* b_scales_dev, float* expert_scales_dev, void* workspace_dev, size_t workspace_bytes,
+                      void* stream) {
+  int st = check_fp4(b_scale_format, E, N, K);
+  if (st != W4A8_OK) return st;
+  const bool nv = b_scale_format == W4A8_WSCALE_NV;
+  if (!nv && expert_scales_dev) return fail(W4A8_ERR_LAYOUT, "expert scales go with NVFP4 only");
+  if (N > 0 && (!w_bf16_dev || !B_fp4_dev || !b_scales_dev || (nv && (!expert_scales_dev || !workspace_dev))))
+    return fail(W4A8_ERR_NULL, "null pointer argument");
+  if (!aligned(w_bf16_dev, 16) || !aligned(B_fp4_dev, 16) || !aligned(expert_scales_dev, 4) ||
+      !aligned(workspace_dev, 4))
+    return fail(W4A8_ERR_ALIGN, "w and B need 16-byte, expert scales and workspace 4-byte alignment");
+  if (workspace_bytes < w4a8_quantize_fp4_bytes(b_scale_format, E, N, K))
+    return fail(W4A8_ERR_CAPACITY, "workspace of %zu bytes, %zu needed", workspace_bytes,
+                w4a8_quantize_fp4_bytes(b_scale_format, E, N, K));
+  const DeviceInfo* d = nullptr;
+  st = device_info(&d);
+  if (st != W4A8_OK) return st;
+  if (N == 0) return ok();
+  hipError_t e = w4a8::launch_quant_fp4(w_bf16_dev, nv, E, N, K, B_fp4_dev, b_scales_dev, expert_scales_dev,
+                                        static_cast<uint32_t*>(workspace_dev), (hipStream_t)stream);
+  if (e != hipSuccess) return fail(W4A8_ERR_HIP, "quantize_fp4 launch: %s", hipGetErrorString(e));
+  return ok();
+}
+
+int w4a8_dequantize_fp4(const uint8_t* B_fp4_dev, const uint8_t* b_scales_dev, int b_scale_format,
+                        const float* expert_scales_dev, int E, int N, int K, uint16_t* w_bf16_dev, void* stream) {
+  int st = check_fp4(b_scale_format, E, N, K);
+  if (st != W4A8_OK) return st;
+  if (N > 0 && (!w_bf16_dev || !B_fp4_dev || !b_scales_dev)) return fail(W4A8_ERR_NULL, "null pointer argument");
+  if (!aligned(w_bf16_dev, 16) || !aligned(B_fp4_dev, 16) || !aligned(expert_scales_dev, 4))
+    return fail(W4A8_ERR_ALIGN, "w and B need 16-byte, expert scales 4-byte alignment");
+  const DeviceInfo* d = nullptr;
+  st = device_info(&d);
+  if (st != W4A8_OK) return st;
+  if (N == 0) return ok();
+  hipError_t e = w4a8::launch_dequant_fp4(B_fp4_dev, b_scales_dev, b_scale_format == W4A8_WSCALE_NV,
+                                          expert_scales_dev, E, N, K, w_bf16_dev, (hipStream_t)stream);
+  if (e != hipSuccess) return fail(W4A8_ERR_HIP, "dequantize_fp4 launch: %s", hipGetErrorString(e));
+  return ok();
+}
+
+int w4a8_quantize_gather_fp4(const uint16_t* x_bf16_dev, int T, int K, const int32_t* row_of_slot_dev, int top_k,
+                             int R, uint8_t* A_fp4_dev, uint8_t* a_scales_dev, void* stream) {
+  int st = check_slots(T, top_k, R, K, "K");
+  if (st != W4A8_OK) return st;
+  if (K % 32 || K > W4A8_MAX_K)
+    return fail(W4A8_ERR_SHAPE, "K=%d must be a multiple of 32 in [32, %d]", K, W4A8_MAX_K);
+  if (T > 0 && (!x_bf16_dev || !row_of_slot_dev || (R > 0 && (!A_fp4_dev || !a_scales_dev))))
+    return fail(W4A8_ERR_NULL, "null pointer argument");
+  if (!aligned(x_bf16_dev, 16) || !aligned(A_fp4_dev, 16) || !aligned(row_of_slot_dev, 4))
+    return fail(W4A8_ERR_ALIGN, "x and A need 16-byte, row_of_slot 4-byte alignment");
+  const DeviceInfo* d = nullptr;
+  st = device_info(&d);
+  if (st != W4A8_OK) return st;
+  if (T == 0 || R == 0) return ok();
+  hipError_t e = w4a8::launch_quant_gather_fp4(x_bf16_dev, T, K, row_of_slot_dev, top_k, R, A_fp4_dev, a_scales_dev,
+                                               (hipStream_t)stream);
+  if (e != hipSuccess) return fail(W4A8_ERR_HIP, "quantize_gather_fp4 launch: %s", hipGetErrorString(e));
+  return ok();
+}
+
+int w4a8_grouped_gemm_a4(const uint8_t* A_fp4_dev, const uint8_t* a_scales_dev, const uint8_t* B_fp4_dev,
+                         const uint8_t* b_scales_dev, const int32_t* expert_offsets_dev, int R, int E, int N, int K,
+                         uint16_t* C_bf16_dev, void* stream) {
+  int st = check_gemm_shape(E, N, K);
+  if (st != W4A8_OK) return st;
+  if (R < 0) return fail(W4A8_ERR_SHAPE, "R=%d", R);
+  if (R > 0 && (!A_fp4_dev || !a_scales_dev || !B_fp4_dev || !b_scales_dev || !expert_offsets_dev || !C_bf16_dev))
+    return fail(W4A8_ERR_NULL, "null pointer argument");
+  if (!aligned(A_fp4_dev, 16) || !aligned(B_fp4_dev, 16) || !aligned(C_bf16_dev, 16) || !aligned(a_scales_dev, 4) ||
+      !aligned(b_scales_dev, 4) || !aligned(expert_offsets_dev, 4))
+    return fail(W4A8_ERR_ALIGN, "A, B, C need 16-byte and scales/offsets 4-byte alignment");
+  const DeviceInfo* d = nullptr;
+  st = device_info(&d);
+  if (st != W4A8_OK) return st;
+  if (R == 0) return ok();
+  const w4a8::TileArgs args{A_fp4_dev, B_fp4_dev, a_scales_dev, b_scales_dev, expert_offsets_dev, C_bf16_dev,
+                            E, R, N, K, 0};
+  hipError_t e = w4a8::launch_grouped_a4(args, (hipStream_t)stream);
+  if (e != hipSuccess) return fail(W4A8_ERR_HIP, "grouped_gemm_a4 launch: %s", hipGetErrorString(e));
+  return ok();
+}
+
+size_t w4a8_clip_grads_bytes(const int64_t* numel_host, int n) {
+  if (n < 0 || n > kMaxGrads || (n > 0 && !numel_host)) return 0;
+  int64_t total = 0;
+  for (int i = 0; i < n; ++i) {
+    if (numel_host[i] < 0 || numel_host[i] >= kMaxGradElements) return 0;
+    total += numel_host[i];
+  }
+  if (total >= kMaxGradElements) return 0;
+  return (size_t)(w4a8::grad_norm_parts(numel_host, n) + 1) * sizeof(double);
+}
+
+int w4a8_clip_grads(const void* const* tensors_host, void* const* outs_host, const int64_t* numel_host,
+                    const int* types_host, int n, float max_norm, float eps, void* workspace_dev,
+                    size_t workspace_bytes, float* norm_dev, void* stream) {
+  if (n < 0 || n > kMaxGrads) return fail(W4A8_ERR_SHAPE, "n=%d tensors outside [0, %d]", n, kMaxGrads);
+  if ((n > 0 && (!tensors_host || !numel_host || !types_host)) || !workspace_dev || !norm_dev)
+    return fail(W4A8_ERR_NULL, "null pointer argument");
+  if (!(max_norm >= 0.0f) || !(eps >= 0.0f)) return fail(W4A8_ERR_SHAPE, "max_norm and eps must not be negative or NaN");
+  const size_t need = w4a8_clip_grads_bytes(numel_host, n);
+  if (need == 0) return fail(W4A8_ERR_SHAPE, "a negative number of elements, or 2^44 and more in all");
+  for (int i = 0; i < n; ++i) {
+    if (types_host[i] != W4A8_TYPE_F32 && types_host[i] != W4A8_TYPE_BF16)
+      return fail(W4A8_ERR_LAYOUT, "types[%d]=%d is neither fp32 (0) nor bf16 (1)", i, types_host[i]);
+    if (numel_host[i] == 0) continue;
+    const size_t a = types_host[i] == W4A8_TYPE_F32 ? 4 : 2;
+    if (!tensors_host[i] || (outs_host && !outs_host[i])) return fail(W4A8_ERR_NULL, "tensor %d is null", i);
+    if (!aligned(tensors_host[i], a) || (outs_host && !aligned(outs_host[i], a)))
+      return fail(W4A8_ERR_ALIGN, "tensor %d needs the alignment of its type", i);
+  }
+  if (!aligned(workspace_dev, 8) || !aligned(norm_dev, 4))
+    return fail(W4A8_ERR_ALIGN, "workspace needs 8-byte, norm 4-byte alignment");
+  if (workspace_bytes < need)
+    return fail(W4A8_ERR_CAPACITY, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
+  if (outs_host) {
+    const int st = check_outputs_apart(tensors_host, outs_host, numel_host, types_host, n);
+    if (st != W4A8_OK) return st;
+  }
+  const DeviceInfo* d = nullptr;
+  int st = device_info(&d);
+  if (st != W4A8_OK) return st;
+  hipError_t e = w4a8::launch_clip_grads(tensors_host, outs_host, numel_host, types_host, n, max_norm, eps,
+                                         static_cast<double*>(workspace_dev), norm_dev, (hipStream_t)stream);
+  if (e != hipSuccess) return fail(W4A8_ERR_HIP, "clip_grads launch: %s", hipGetErrorString(e));
   return ok();
 }
 

@@ -1,0 +1,296 @@
+// bf16 to 4-bit floating point with group scales and back, gfx950.
+//
+//   MXFP4 (32 along K): e = floor(log2 amax) - 2, scale 2^e as an E8M0 code (1 for a
+//     group of zeros), code = E2M1 of x / 2^e
+//   NVFP4 (16 along K): gs = amax of the expert / (6 * 448) in fp32 (1 for zeros),
+//     s = E4M3(amax of the group / (6 gs)), code = E2M1 of x / (s gs)
+// All roundings to nearest, halves to even, past 6 to 6: the codes are those of
+// the exact quotients.  MX divides by powers of two, which is exact.  NV's
+// quotients meet the grids' midpoints exactly when x and the amax share their
+// mantissas, and come as near as 2^-33 to them otherwise (x has 8 significant
+// bits, s 4, gs 24, a midpoint 3): both are told apart in 64 bits.
+//
+// A stream: a thread holds 16 columns, i.e. an NVFP4 group, two threads an MX
+// group.
+#include "swiglu.h"
+#include "w4a8_launch.h"
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+namespace w4a8 {
+namespace {
+
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+typedef float v2f __attribute__((ext_vector_type(2)));
+typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+
+constexpr int Q_THREADS = 256;
+constexpr float kScaleFloor = 7.888609052210118e-31f;  // 2^-100
+
+struct Cols { v4u lo, hi; };   // 16 bf16 columns
+__device__ __forceinline__ Cols load16(const uint16_t* p) {
+  const v4u* q = reinterpret_cast<const v4u*>(p);
+  return {q[0], q[1]};
+}
+__device__ __forceinline__ float col(const Cols& c, int i) {
+  const uint32_t w = i < 8 ? c.lo[i >> 1] : c.hi[(i - 8) >> 1];
+  return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
+}
+// The bits of max |x| of the 16 columns; infinity or NaN come out above 0x7f7f....
+__device__ __forceinline__ uint32_t amax_bits(const Cols& c) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    m = max(m, max((c.lo[i] << 16) & 0x7fffffffu, c.lo[i] & 0x7fff0000u));
+    m = max(m, max((c.hi[i] << 16) & 0x7fffffffu, c.hi[i] & 0x7fff0000u));
+  }
+  return m;
+}
+constexpr uint32_t INF_BITS = 0x7f800000u;
+
+// The codes and the scale of half an MX group; the other half is in the
+// neighbouring lane (lane ^ 1).  A group with an infinity or a NaN gets the NaN
+// scale.
+__device__ __forceinline__ v2u mx_codes(const Cols& c, uint8_t& scale) {
+  uint32_t m = amax_bits(c);
+  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xb1, 0xf, 0xf, true));   // quad_perm 1 0 3 2
+  if (m >= INF_BITS) {
+    scale = 0xff;
+    return (v2u){0u, 0u};
+  }
+  int e = m ? __builtin_amdgcn_frexp_expf(__uint_as_float(m)) - 3 : 0;
+  e = e < -127 ? -127 : e;   // 125 at most
+  scale = (uint8_t)(e + 127);
+  v2u q;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t w = 0;
+#define W4A8_FP4(B)                                                                                           \
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, ldexpf(col(c, 8 * h + 2 * B), -e),                          \
+                                               ldexpf(col(c, 8 * h + 2 * B + 1), -e), 1.0f, B)
+    W4A8_FP4(0);
+    W4A8_FP4(1);
+    W4A8_FP4(2);
+    W4A8_FP4(3);
+#undef W4A8_FP4
+    q[h] = w;
+  }
+  return q;
+}
+
+// Rows of bf16 to MXFP4 in place order: unit i holds columns 16 i .. 16 i + 15
+// of the whole array (K % 32 == 0, so a pair of units is a group).
+__global__ void __launch_bounds__(Q_THREADS)
+quant_mx_kernel(const uint16_t* __restrict__ x, int64_t unit0, int64_t units, uint8_t* __restrict__ B,
+                uint8_t* __restrict__ SB) {
+  const int64_t i = unit0 + (int64_t)blockIdx.x * Q_THREADS + threadIdx.x;
+  if (i >= units) return;   // units is even: a pair of lanes leaves together
+  uint8_t s;
+  const v2u q = mx_codes(load16(x + i * 16), s);
+  *reinterpret_cast<v2u*>(B + i * 8) = q;
+  if (!(i & 1)) SB[i >> 1] = s;
+}
+
+// Tokens to the grouped rows of their slots: a workgroup per token.
+__global__ void __launch_bounds__(Q_THREADS)
+quant_gather_mx_kernel(const uint16_t* __restrict__ x, int K, const int32_t* __restrict__ row_of_slot, int top_k,
+                       int R, uint8_t* __restrict__ A, uint8_t* __restrict__ SA) {
+  const int64_t t = blockIdx.x;
+  const int32_t* rs = row_of_slot + t * top_k;
+  for (int u = threadIdx.x; u < K / 16; u += blockDim.x) {
+    uint8_t s;
+    const v2u q = mx_codes(load16(x + t * K + u * 16), s);
+    for (int j = 0; j < top_k; ++j) {
+      const int r = rs[j];
+      if (r < 0 || r >= R) continue;   // a slot that names no row
+      *reinterpret_cast<v2u*>(A + (size_t)r * (K / 2) + u * 8) = q;
+      if (!(u & 1)) SA[(size_t)r * (K / 32) + (u >> 1)] = s;
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t block_max(uint32_t m, uint32_t* s) {
+#pragma unroll
+  for (int d = 32; d; d >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d, 64));
+  if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = m;
+  __syncthreads();
+  for (int w = 0; w < (int)(blockDim.x >> 6); ++w) m = max(m, s[w]);
+  return m;
+}
+
+// Largest finite |x| of a part of an expert, as bits: partials[e][part].
+__global__ void __launch_bounds__(Q_THREADS)
+expert_amax_kernel(const uint16_t* __restrict__ x, int64_t units, int parts, int64_t b0,
+                   uint32_t* __restrict__ partials) {
+  __shared__ uint32_t s[Q_THREADS / 64];
+  const int64_t b = b0 + blockIdx.x, e = b / parts;
+  const uint16_t* xe = x + e * units * 16;
+  uint32_t m = 0;
+  for (int64_t u = (b - e * parts) * Q_THREADS + threadIdx.x; u < units; u += (int64_t)parts * Q_THREADS) {
+    const Cols c = load16(xe + u * 16);
+    uint32_t v = amax_bits(c);
+    if (v >= INF_BITS) {   // rare: again, without what is not finite
+      v = 0;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint32_t a = __float_as_uint(col(c, i)) & 0x7fffffffu;
+        v = max(v, a < INF_BITS ? a : 0u);
+      }
+    }
+    m = max(m, v);
+  }
+  m = block_max(m, s);
+  if (threadIdx.x == 0) partials[b] = m;
+}
+
+// v rounded to a multiple of u (a power of two), halves to even; |v| < 2^50 u.
+__device__ __forceinline__ double round_to(double v, double u) {
+  const double c = 6755399441055744.0 * u;   // 1.5 * 2^52
+  return (v + c) - c;
+}
+
+__global__ void __launch_bounds__(Q_THREADS)
+quant_nv_kernel(const uint16_t* __restrict__ x, int64_t units, int64_t per_expert, int64_t b0, int parts,
+                const uint32_t* __restrict__ partials, uint8_t* __restrict__ B, uint8_t* __restrict__ SB,
+                float* __restrict__ gs) {
+  __shared__ uint32_t sm[Q_THREADS / 64];
+  const int64_t b = b0 + blockIdx.x, e = b / per_expert;
+  const int64_t u = (b - e * per_expert) * Q_THREADS + threadIdx.x;
+  uint32_t m = 0;
+  for (int p = threadIdx.x; p < parts; p += Q_THREADS) m = max(m, partials[e * parts + p]);
+  m = block_max(m, sm);
+  // below 2^-100 a scale of the fp32 range would lose its bits: such experts count as zeros
+  const float g = __uint_as_float(m) >= kScaleFloor ? __fdiv_rn(__uint_as_float(m), 2688.0f) : 1.0f;
+  if (b == e * per_expert && threadIdx.x == 0) gs[e] = g;
+  if (u >= units) return;
+  const int64_t i = e * units + u;
+  const Cols c = load16(x + i * 16);
+  const uint32_t am = amax_bits(c);
+  v2u q = {0u, 0u};
+  uint32_t code = 0x7f;   // NaN: a group with an infinity or a NaN
+  if (am < INF_BITS) {
+    // E4M3 of r in [0, 448 (1 + 2^-24)]: steps of 2^(floor(log2 r) - 3), of 2^-9 below 2^-6
+    const double r = (double)__uint_as_float(am) / (6.0 * (double)g);
+    int ex = r > 0.0 ? __builtin_amdgcn_frexp_exp(r) - 1 : -6;
+    ex = ex < -6 ? -6 : ex;
+    const double s = round_to(r, ldexp(1.0, ex - 3));
+    const double t = s * (double)g;   // exact: 28 bits
+    // the code of s: s is 0 or a number of E4M3, which the conversion keeps
+    code = __builtin_amdgcn_cvt_pk_fp8_f32((float)s, 0.0f, 0, false) & 0xff;
+    if (s > 0.0) {
+      const double inv = 1.0 / t;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const float xf = col(c, j);
+        // within 2^-51 of |x| / t; a true midpoint is a multiple of 2^-40 and is
+        // restored by rounding to one, everything else is 2^-33 off
+        const double v = round_to(fabs((double)xf) * inv, 0x1p-40);
+        // the grid: steps of 1/2 up to 2, 1 up to 4, 2 up to 6
+        const double y = round_to(v, v < 2.0 ? 0.5 : v < 4.0 ? 1.0 : 2.0);
+        const float yf = fminf((float)y, 6.0f);
+        const float a = yf < 2.0f ? yf * 2.0f : yf < 4.0f ? yf + 2.0f : fmaf(yf, 0.5f, 4.0f);
+        const uint32_t k = (uint32_t)a | ((__float_as_uint(xf) >> 28) & 8u);
+        q[j >> 3] |= k << (4 * (j & 7));
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) q[j >> 3] |= ((__float_as_uint(col(c, j)) >> 28) & 8u) << (4 * (j & 7));
+    }
+  }
+  *reinterpret_cast<v2u*>(B + i * 8) = q;
+  SB[i] = (uint8_t)code;
+}
+
+// Codes to bf16: a thread decodes 8 columns.  value = bf16((code * s) gs), code
+// * s exact in fp32.
+template <bool NV>
+__global__ void __launch_bounds__(Q_THREADS)
+dequant_kernel(const uint8_t* __restrict__ B, const uint8_t* __restrict__ SB, const float* __restrict__ gs,
+               int64_t units, int64_t per_expert, int64_t b0, uint16_t* __restrict__ out) {
+  const int64_t b = b0 + blockIdx.x, e = b / per_expert;
+  const int64_t u = (b - e * per_expert) * Q_THREADS + threadIdx.x;
+  if (u >= units) return;
+  const int64_t i = e * units + u;
+  const uint32_t q = *reinterpret_cast<const uint32_t*>(B + i * 4);
+  const float g = gs ? gs[e] : 1.0f;
+  const uint32_t sc = SB[NV ? i >> 1 : i >> 2];
+  const float s = NV ? __builtin_amdgcn_cvt_f32_fp8((int)sc, 0) : 1.0f;
+  const int ex = (int)sc - 127;
+  const bool nan = !NV && sc == 0xff;
+  v4u o;
+#define W4A8_DEQ(J)                                                                                   \
+  {                                                                                                   \
+    v2f v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, J);                                     \
+    v[0] = (NV ? v[0] * s : ldexpf(v[0], ex)) * g;                                                    \
+    v[1] = (NV ? v[1] * s : ldexpf(v[1], ex)) * g;                                                    \
+    if (nan) v[0] = v[1] = __builtin_nanf("");                                                        \
+    o[J] = __builtin_bit_cast(uint32_t, __builtin_convertvector(v, v2bf));                            \
+  }
+  W4A8_DEQ(0)
+  W4A8_DEQ(1)
+  W4A8_DEQ(2)
+  W4A8_DEQ(3)
+#undef W4A8_DEQ
+  *reinterpret_cast<v4u*>(out + i * 8) = o;
+}
+
+// Parts of an expert's amax: enough workgroups for the chip over all experts,
+// few enough for every quantising workgroup to read them.
+int amax_parts(int E, int64_t units) {
+  const int64_t most = std::max<int64_t>(1, std::min<int64_t>(256, 2048 / E));
+  return (int)std::min<int64_t>(most, (units + Q_THREADS - 1) / Q_THREADS);
+}
+
+}  // namespace
+
+size_t quant_fp4_workspace(bool nv, int E, int N, int K) {
+  return nv ? (size_t)E * amax_parts(E, (int64_t)N * (K / 16)) * sizeof(uint32_t) : 0;
+}
+
+hipError_t launch_quant_fp4(const uint16_t* x, bool nv, int E, int N, int K, uint8_t* B, uint8_t* SB, float* gs,
+                            uint32_t* work, hipStream_t stream) {
+  const int64_t units = (int64_t)N * (K / 16);
+  if (!nv) {
+    const int64_t all = units * E;
+    return in_launches((all + Q_THREADS - 1) / Q_THREADS, Q_THREADS, [&](int64_t b, int64_t n) {
+      hipLaunchKernelGGL(quant_mx_kernel, dim3((unsigned)n), dim3(Q_THREADS), 0, stream, x, b * Q_THREADS, all, B, SB);
+    });
+  }
+  const int parts = amax_parts(E, units);
+  hipError_t e = in_launches((int64_t)E * parts, Q_THREADS, [&](int64_t b, int64_t n) {
+    hipLaunchKernelGGL(expert_amax_kernel, dim3((unsigned)n), dim3(Q_THREADS), 0, stream, x, units, parts, b, work);
+  });
+  if (e != hipSuccess) return e;
+  const int64_t per = (units + Q_THREADS - 1) / Q_THREADS;
+  return in_launches(per * E, Q_THREADS, [&](int64_t b, int64_t n) {
+    hipLaunchKernelGGL(quant_nv_kernel, dim3((unsigned)n), dim3(Q_THREADS), 0, stream, x, units, per, b, parts, work,
+                       B, SB, gs);
+  });
+}
+
+hipError_t launch_dequant_fp4(const uint8_t* B, const uint8_t* SB, bool nv, const float* gs, int E, int N, int K,
+                              uint16_t* out, hipStream_t stream) {
+  const int64_t units = (int64_t)N * (K / 8), per = (units + Q_THREADS - 1) / Q_THREADS;
+  return in_launches(per * E, Q_THREADS, [&](int64_t b, int64_t n) {
+    if (nv)
+      hipLaunchKernelGGL(dequant_kernel<true>, dim3((unsigned)n), dim3(Q_THREADS), 0, stream, B, SB, gs, units, per, b,
+                         out);
+    else
+      hipLaunchKernelGGL(dequant_kernel<false>, dim3((unsigned)n), dim3(Q_THREADS), 0, stream, B, SB, gs, units, per,
+                         b, out);
+  });
+}
+
+hipError_t launch_quant_gather_fp4(const uint16_t* x, int T, int K, const int32_t* row_of_slot, int top_k, int R,
+                                   uint8_t* A, uint8_t* SA, hipStream_t stream) {
+  const int threads = std::min(Q_THREADS, (K / 16 + 63) / 64 * 64);
+  return in_launches(T, threads, [&](int64_t t, int64_t n) {
+    hipLaunchKernelGGL(quant_gather_mx_kernel, dim3((unsigned)n), dim3(threads), 0, stream, x + t * K, K,
+                       row_of_slot + t * top_k, top_k, R, A, SA);
+  });
+}
+
+}  // namespace w4a8

@@ -98,4 +98,62 @@ hipError_t launch_swiglu(const uint16_t* C, int R, int I, uint16_t* h, uint8_t* 
 hipError_t launch_swiglu_backward(const uint8_t* codes, const float* scales, const uint16_t* dh, int R, int I,
                                   uint16_t* dC, uint16_t* h, hipStream_t stream);
 
+struct NormArgs {
+  const uint16_t* x;       // [T][K] bf16
+  const uint16_t* res;     // [T][K] or null
+  const void* w;           // [K] bf16 or fp32, or null (ones)
+  uint16_t* y;             // [T][K] or null
+  uint16_t* h;             // [T][K] x + res, or null
+  uint8_t* A;              // [T][K] E4M3 codes of y, or null
+  float* SA;               // per (row, 128 columns), layout 0 row-major, 1 M-major
+  int T, K, w_f32, layout;
+  float eps;
+};
+struct NormGradArgs {
+  const uint16_t* h;       // [T][K]
+  const uint16_t* dy;      // [T][K]
+  const uint16_t* dres;    // [T][K] or null
+  const void* w;           // [K] or null
+  uint16_t* dx;            // [T][K]
+  float* dw;               // [K] or null
+  float* partials;         // [norm_backward_parts(T)][K]
+  int T, K, w_f32;
+  float eps;
+};
+constexpr int NORM_PARTS = 1024;   // most workgroups of the gradient, each with a part of dw
+int norm_backward_parts(int T);
+hipError_t launch_rms_norm(const NormArgs& args, hipStream_t stream);
+hipError_t launch_rms_norm_backward(const NormGradArgs& args, hipStream_t stream);
+
+// Gradient norm: workgroups of a launch at most, each with one partial sum; the
+// workspace holds grad_norm_parts() + 1 of them.
+constexpr int GN_GRID = 1024;
+int grad_norm_parts(const int64_t* numel, int n);
+hipError_t launch_clip_grads(const void* const* in, void* const* out, const int64_t* numel, const int* types, int n,
+                             float max_norm, float eps, double* partials, float* norm, hipStream_t stream);
+
+size_t quant_fp4_workspace(bool nv, int E, int N, int K);
+hipError_t launch_quant_fp4(const uint16_t* x, bool nv, int E, int N, int K, uint8_t* B, uint8_t* SB, float* gs,
+                            uint32_t* work, hipStream_t stream);
+hipError_t launch_dequant_fp4(const uint8_t* B, const uint8_t* SB, bool nv, const float* gs, int E, int N, int K,
+                              uint16_t* out, hipStream_t stream);
+hipError_t launch_quant_gather_fp4(const uint16_t* x, int T, int K, const int32_t* row_of_slot, int top_k, int R,
+                                   uint8_t* A, uint8_t* SA, hipStream_t stream);
+
+// The tiled products out[y, x] = sum over z: rows (or N of the weights' gradient)
+// along y, weights (or K) along x.
+struct TileArgs {
+  const uint8_t* Y;        // A, dC: rows
+  const uint8_t* X;        // W, or A for the weights' gradient
+  const uint8_t* SY;       // E8M0 codes of FP4 rows [R][K/32] and weights [E][N][K/32]
+  const uint8_t* SX;
+  const int32_t* offsets;  // [E+1]
+  void* out;
+  int E, R, N, K, accumulate;
+};
+hipError_t launch_grouped_bf16(const TileArgs& args, hipStream_t stream);
+hipError_t launch_grouped_dgrad(const TileArgs& args, hipStream_t stream);
+hipError_t launch_grouped_wgrad(const TileArgs& args, bool f32, hipStream_t stream);
+hipError_t launch_grouped_a4(const TileArgs& args, hipStream_t stream);
+
 }  // namespace w4a8

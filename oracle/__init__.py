@@ -34,6 +34,10 @@ Modules:
              and of the combine.
   matvec  -- products of a few tokens with 4-bit weights and group scales.
   swiglu8 -- SwiGLU's 8-bit input copy, and the gradient from it.
+  norm    -- root-mean-square norm with residual, its 8-bit output and gradient.
+  fp4     -- bf16 to MXFP4 and NVFP4 and back.
+  grouped -- grouped products with given values, their gradients, and gradient
+             clipping.
 
 Parity status: no page prints a worked example or output value for any of
 these, so every function is pinned by closed forms, invariants, exact
@@ -60,3 +64,4 @@ from .gate import topk_gate_backward_f64, topk_gate_f64  # noqa: F401
 from .moves import combine_backward_ref, dispatch_backward_ref, dispatch_ref  # noqa: F401
 from .matvec import FMT_INT4, matvec_f64  # noqa: F401
 from .swiglu8 import checkpoint_ref, decode_f64, swiglu_backward_f64  # noqa: F401
+from . import fp4, grouped, norm  # noqa: F401
