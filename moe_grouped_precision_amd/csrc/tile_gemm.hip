@@ -25,6 +25,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 namespace w4a8 {
 namespace {
@@ -34,8 +35,6 @@ typedef short v4s __attribute__((ext_vector_type(4)));
 typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 
 enum { FWD = 0, ROWS = 1, WEIGHTS = 2, FOUR = 3 };
-constexpr int STEP = 64;     // bytes of z per row and step
-constexpr int ZROWS = 32;    // rows of z per step of a transposed operand
 
 // What a chunk past the end of z is read from: zeros, so that whatever the
 // buffer holds there (another expert's rows, infinities) stays out of the sums.
@@ -62,22 +61,39 @@ __device__ __forceinline__ int swz(int z) {
   return 2 * ((z & 3) | ((z >> 1) & 4)) & (T / 8 - 1);
 }
 
-// Fragment of 16 rows of an operand with contiguous z: lane 16 q + i holds
-// 16 bytes, chunk q of row i.
-__device__ __forceinline__ v4i frag_rows(uint32_t tile, int blk, int lane) {
-  const int i = lane & 15, q = lane >> 4;
-  return *(lds_v4i*)(uintptr_t)(tile + (blk * 16 + i) * STEP + ((q ^ (i >> 2)) << 4));
+// Place of the chunks of a row with contiguous z.  A 16-byte read of a wave is
+// served in passes of 16 lanes over all banks, lanes 0-3, 12-15, 20-27 and the
+// others of each half; these keys put 16 different places in each.
+template <int KS>
+__device__ __forceinline__ int key(int row) {
+  return KS == 1 ? -(row >> 2) & 3 : (row >> 1) & 7;
 }
-// The same of a transposed one of T columns: lane 16 q + i holds z = 8 q .. 8 q + 7 of
-// column i.
-template <int T>
-__device__ __forceinline__ v4i frag_cols(uint32_t tile, int blk, int lane) {
+// Fragment h of row block blk of an operand whose tile lies at `tile`: lane 16 q +
+// i holds 16 bytes, chunk 4 h + q of row i.  (A pointer and a constant, so that
+// the block goes into the instruction's offset.)
+template <int KS>
+__device__ __forceinline__ uint32_t rows_base(uint32_t tile, int h, int lane) {
   const int i = lane & 15, q = lane >> 4;
-  const int z = 8 * q + (i >> 2), chunk = 2 * blk + ((i >> 1) & 1), in = (i & 1) * 8;
-  const uint32_t a0 = tile + z * (T * 2) + ((chunk ^ swz<T>(z)) << 4) + in;
+  return tile + i * (64 * KS) + (((4 * h + q) ^ key<KS>(i)) << 4);
+}
+template <int KS>
+__device__ __forceinline__ v4i frag_rows(uint32_t base, int blk) {
+  return *(lds_v4i*)((lds_u8*)(uintptr_t)base + blk * 16 * (64 * KS));
+}
+// The same of a transposed one of T columns: lane 16 q + i holds z = 32 h + 8 q ..
+// 8 q + 7 of column i.  The block's low bits meet swz's in the chunk's number.
+template <int T>
+__device__ __forceinline__ uint32_t cols_base(int lane) {   // of a tile at 0, block 0
+  const int i = lane & 15, q = lane >> 4, z = 8 * q + (i >> 2);
+  return z * (T * 2) + ((((i >> 1) & 1) ^ swz<T>(z)) << 4) + (i & 1) * 8;
+}
+template <int T>
+__device__ __forceinline__ v4i frag_cols(uint32_t base, uint32_t tile, int blk, int h) {
+  constexpr int LOW = T / 16 < 8 ? T / 16 - 1 : 7;
+  lds_u8* p = (lds_u8*)(uintptr_t)(tile + (base ^ ((blk & LOW) << 5))) + (blk & ~LOW) * 32 + h * 32 * (T * 2);
   // z + 4 has the same place: swz looks at bits 0, 1 and 3
-  const v2u lo = __builtin_bit_cast(v2u, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(uintptr_t)a0));
-  const v2u hi = __builtin_bit_cast(v2u, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(uintptr_t)(a0 + 4 * T * 2)));
+  const v2u lo = __builtin_bit_cast(v2u, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)p));
+  const v2u hi = __builtin_bit_cast(v2u, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(p + 4 * T * 2)));
   return (v4i){(int)lo[0], (int)lo[1], (int)hi[0], (int)hi[1]};
 }
 
@@ -101,18 +117,24 @@ __device__ __forceinline__ bool find_tile(const TileArgs& a, int64_t b, Place& p
   for (int i = lane; i < a.E; i += 64) {
     const int o0 = a.offsets[i], o1 = a.offsets[i + 1];
     bad |= o1 < o0 || (i == 0 && o0 != 0) || (i == a.E - 1 && o1 > a.R);
-    sum += MODE == WEIGHTS ? fixed : (int)((uint32_t)(o1 - o0 + TY - 1) / TY);
+    if (MODE != WEIGHTS) sum += (int)((uint32_t)(o1 - o0 + TY - 1) / TY);
   }
   if (__ballot(bad)) return false;
-  const int64_t total = (int64_t)__builtin_amdgcn_readlane(wave_inclusive_sum(sum), 63) * nt;
-  const int64_t per = (total + 7) >> 3, t = (b & 7) * per + (b >> 3);
-  if ((b >> 3) >= per || t >= total) return false;
-  int m = (int)(t / nt);   // row tiles before the expert's are whole rows of nt tiles
-  int e = 0, mine = fixed;
+  int64_t t;
+  int m = 0, e = 0, mine = fixed;
   if (MODE == WEIGHTS) {
-    e = m / fixed;
-    m = e * fixed;
+    // a tile costs what its expert has rows: every XCD gets an eighth of each expert
+    const int all = fixed * nt, per = (all + 7) >> 3;
+    const int64_t j = b >> 3;
+    e = (int)(j / per);
+    t = (b & 7) * per + (j - (int64_t)e * per);
+    if (e >= a.E || t >= all) return false;
   } else {
+    const int64_t total = (int64_t)__builtin_amdgcn_readlane(wave_inclusive_sum(sum), 63) * nt;
+    const int64_t per = (total + 7) >> 3;
+    t = (b & 7) * per + (b >> 3);
+    if ((b >> 3) >= per || t >= total) return false;
+    m = (int)(t / nt);   // row tiles before the expert's are whole rows of nt tiles
     int before = 0;
     for (int base = 0;; base += 64) {
       const int i = base + lane;
@@ -135,8 +157,16 @@ __device__ __forceinline__ bool find_tile(const TileArgs& a, int64_t b, Place& p
   p.e = uniform(e);
   p.r0 = uniform(a.offsets[p.e]);
   p.rows = uniform(a.offsets[p.e + 1]) - p.r0;
-  p.y0 = uniform(yt) * TY;
-  p.ny = min(TY, (MODE == WEIGHTS ? a.N : p.rows) - p.y0);
+  if (MODE == WEIGHTS) {
+    p.y0 = uniform(yt) * TY;
+    p.ny = min(TY, a.N - p.y0);
+  } else {
+    // an expert's rows in equal tiles of whole blocks of 16: the kernel leaves
+    // out blocks that a tile does not have
+    const int per = ((p.rows + mine - 1) / mine + 15) & ~15;
+    p.y0 = uniform(yt * per);
+    p.ny = uniform(min(per, p.rows - p.y0));
+  }
   p.x0 = uniform(xt) * TX;
   p.nx = min(TX, width - p.x0);
   return true;
@@ -157,241 +187,391 @@ __device__ __forceinline__ v4i load_any(const uint8_t* p, int n) {
   return v;
 }
 
-// TY x TX tiles, WY x WX waves, NS steps of the operands in LDS.  DIRECT: rows
-// are whole 16-byte chunks at 16-byte addresses and go straight to LDS;
-// otherwise through registers.
-template <int MODE, int TY, int TX, int WY, int WX, int NS, bool DIRECT, typename OUT>
-struct Tile {
+// A lane's 16 bytes of load j (1 KB of LDS, so 64 KS bytes of 16 / KS rows or T columns
+// of rows of z) of an operand: its row, or row of z, and its chunk.
+template <int T, bool TR, int KS>
+__device__ __forceinline__ void chunk_of(int j, int lane, int& row, int& chunk) {
+  constexpr int CPR = TR ? T / 8 : 4 * KS;
+  row = j * (64 / CPR) + lane / CPR;
+  chunk = (lane % CPR) ^ (TR ? swz<T>(row) : key<KS>(row & 15));
+}
+
+// What the kernels of one product have in common.
+template <int MODE>
+struct Operands {
   static constexpr bool YT = MODE == WEIGHTS, XT = MODE == WEIGHTS || MODE == ROWS;   // transposed operands
-  static constexpr int NW = WY * WX, THREADS = 64 * NW;
-  static constexpr int MY = TY / WY / 16, MX = TX / WX / 16;
-  static constexpr int IY = TY / 16 / NW, IX = TX / 16 / NW, NI = IY + IX;   // loads of 1 KB per wave and step
-  static constexpr int SCALES = MODE == FOUR ? (TY + TX) * 4 : 0;
-  static constexpr int SY = MODE == FOUR ? (TY / 64 + NW - 1) / NW : 0, SX = MODE == FOUR ? (TX / 64 + NW - 1) / NW : 0;
-  static constexpr int STAGE = (TY + TX) * STEP + SCALES;
-  static constexpr int LDS = STAGE * NS;
-  static constexpr int PER = NI + SY + SX;
-  static_assert(TY / 16 % NW == 0 && TX / 16 % NW == 0, "whole loads per wave");
-  static_assert(DIRECT || MODE != FOUR, "FP4 rows are whole chunks");
-
-  // This wave's i-th load of a step: its place in the tile and the lane's chunk.
-  template <int T, bool TR>
-  static __device__ __forceinline__ void chunk_of(int j, int lane, int& row, int& chunk) {
-    if (TR) {
-      constexpr int CPR = T / 8;
-      row = j * (64 / CPR) + lane / CPR;                // z
-      chunk = (lane % CPR) ^ swz<T>(row);               // of 8 columns
-    } else {
-      row = j * 16 + (lane >> 2);
-      chunk = (lane & 3) ^ ((lane >> 4) & 3);           // of z
-    }
+  const uint8_t *Y, *X;   // of the tile, at z = 0
+  int ybytes, xbytes;     // from row to row
+  int zn;                 // extent of z
+  int width;              // of the output
+  __device__ __forceinline__ Operands(const TileArgs& a, const Place& p) {
+    zn = MODE == WEIGHTS ? p.rows : MODE == ROWS ? a.N : a.K;
+    ybytes = MODE == FOUR ? a.K / 2 : MODE == FWD ? a.K * 2 : a.N * 2;
+    xbytes = MODE == FOUR ? a.K / 2 : a.K * 2;
+    Y = a.Y + (size_t)(p.r0 + (MODE == WEIGHTS ? 0 : p.y0)) * ybytes + (MODE == WEIGHTS ? p.y0 * 2 : 0);
+    X = MODE == WEIGHTS ? a.X + (size_t)p.r0 * xbytes + p.x0 * 2
+        : MODE == ROWS  ? a.X + (size_t)p.e * a.N * xbytes + p.x0 * 2
+                        : a.X + ((size_t)p.e * a.N + p.x0) * xbytes;
+    width = MODE == ROWS || MODE == WEIGHTS ? a.K : a.N;
   }
+};
 
-  static __device__ __forceinline__ void run(const TileArgs& a, int64_t b) {
-    extern __shared__ __align__(1024) uint8_t smem[];
-    const uint32_t lds = lds_u32(smem);
+// The lane's results of one 16 x 16 block to out[y][x .. x+3].
+template <int MODE, bool WHOLE, typename OUT>
+__device__ __forceinline__ void put(const TileArgs& a, const Place& p, int width, int y, int x, v4f v) {
+  if (y >= p.ny || x >= p.nx) return;
+  OUT* o = static_cast<OUT*>(a.out) +
+           (MODE == WEIGHTS ? (size_t)p.e * a.N + p.y0 + y : (size_t)(p.r0 + p.y0 + y)) * width + p.x0 + x;
+  const int n = WHOLE ? 4 : min(4, p.nx - x);
+  if (MODE == WEIGHTS && a.accumulate) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (c < n) v[c] += sizeof(OUT) == 4 ? (float)o[c] : __uint_as_float((uint32_t)(uint16_t)o[c] << 16);
+  }
+  if constexpr (sizeof(OUT) == 4) {
+    if (WHOLE) *reinterpret_cast<v4f*>(o) = v;
+    else
+      for (int c = 0; c < n; ++c) o[c] = v[c];
+  } else {
+    if (WHOLE) store_bf16x4(o, v);
+    else
+      for (int c = 0; c < n; ++c) o[c] = __builtin_bit_cast(uint16_t, (__bf16)v[c]);
+  }
+}
+
+__device__ __forceinline__ v4f mfma_bf16(v4i x, v4i y, v4f acc) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, x), __builtin_bit_cast(v8bf, y), acc, 0, 0, 0);
+}
+
+// ---------------------------------------------------------------------------
+// Rows that are no whole 16-byte chunks at 16-byte addresses: through registers,
+// 128 x 128 tiles, steps of 32 z, two of them in LDS.
+// ---------------------------------------------------------------------------
+template <int MODE, typename OUT>
+struct General {
+  static constexpr int TY = 128, TX = 128, KS = 1, NW = 4, THREADS = 256, M = 4, NI = TY / 16 / NW;
+  static constexpr int STAGE = (TY + TX) * 64, LDS = 2 * STAGE, PER_SIMD = 2;
+
+  static __device__ __forceinline__ void run(const TileArgs& a, int64_t b, uint32_t lds) {
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     Place p;
     if (!find_tile<MODE, TY, TX>(a, b, p)) return;
+    const Operands<MODE> op(a, p);
+    constexpr bool YT = Operands<MODE>::YT, XT = Operands<MODE>::XT;
+    const int steps = (op.zn + 31) / 32;
+    v4f acc[M][M];
+#pragma unroll
+    for (int i = 0; i < M; ++i)
+#pragma unroll
+      for (int j = 0; j < M; ++j) acc[i][j] = (v4f){0.f, 0.f, 0.f, 0.f};
 
-    // operands: base of the tile, bytes from row to row, extent of z
-    const int zn = MODE == WEIGHTS ? p.rows : MODE == ROWS ? a.N : a.K;
-    const int ybytes = MODE == FOUR ? a.K / 2 : MODE == FWD ? a.K * 2 : a.N * 2;
-    const int xbytes = MODE == FOUR ? a.K / 2 : a.K * 2;
-    const uint8_t* Y = a.Y + (size_t)(p.r0 + (MODE == WEIGHTS ? 0 : p.y0)) * ybytes + (MODE == WEIGHTS ? p.y0 * 2 : 0);
-    const uint8_t* X = MODE == WEIGHTS ? a.X + (size_t)p.r0 * xbytes + p.x0 * 2
-                       : MODE == ROWS  ? a.X + (size_t)p.e * a.N * xbytes + p.x0 * 2
-                                       : a.X + ((size_t)p.e * a.N + p.x0) * xbytes;
-    const int steps = MODE == FOUR ? zn / 128 : (zn + 31) / 32;
-    const int full = MODE == FOUR ? steps : zn / 32;   // steps without an end of z in them
+    // the lane's chunks of a step
+    const uint8_t* src[2 * NI];
+    int left[2 * NI];   // z from the chunk on to the end
+    int wide[2 * NI];   // columns of a transposed chunk inside the tile's extent
+#pragma unroll
+    for (int i = 0; i < 2 * NI; ++i) {
+      const bool isy = i < NI;
+      const int j = wave + NW * (i % NI);
+      int row, chunk;
+      if (isy) chunk_of<TY, YT, KS>(j, lane, row, chunk);
+      else chunk_of<TX, XT, KS>(j, lane, row, chunk);
+      const int extent = isy ? p.ny : p.nx, pitch = isy ? op.ybytes : op.xbytes;
+      const uint8_t* base = isy ? op.Y : op.X;
+      if (isy ? YT : XT) {
+        wide[i] = max(0, min(8, extent - chunk * 8));
+        src[i] = base + (size_t)row * pitch + chunk * 16;
+        left[i] = op.zn - row;
+      } else {
+        wide[i] = 8;
+        src[i] = base + (size_t)min(row, extent - 1) * pitch + chunk * 16;
+        left[i] = op.zn - chunk * 8;
+      }
+    }
+    const size_t ystep = YT ? (size_t)32 * op.ybytes : 64, xstep = XT ? (size_t)32 * op.xbytes : 64;
+    v4i reg[2 * NI];
+    auto fetch = [&](int s) {
+#pragma unroll
+      for (int i = 0; i < 2 * NI; ++i) {
+        const int z = left[i] - 32 * s;
+        reg[i] = load_any(src[i], z <= 0 ? 0 : (i < NI ? YT : XT) ? wide[i] : z);
+        src[i] += i < NI ? ystep : xstep;
+      }
+    };
+    auto fill = [&](uint32_t stage) {
+#pragma unroll
+      for (int i = 0; i < 2 * NI; ++i)
+        *(lds_v4i*)(uintptr_t)(stage + (i / NI) * TY * 64 + (wave + NW * (i % NI)) * 1024 + lane * 16) = reg[i];
+    };
+    const int wy = wave >> 1, wx = wave & 1;
+    if (steps > 0) {
+      fetch(0);
+      fill(lds);
+      __syncthreads();
+    }
+    for (int s = 0; s < steps; ++s) {
+      if (s + 1 < steps) fetch(s + 1);
+      const uint32_t stage = lds + (s & 1) * STAGE;
+      v4i fy[M], fx[M];
+#pragma unroll
+      for (int i = 0; i < M; ++i) {
+        fy[i] = YT ? frag_cols<TY>(cols_base<TY>(lane), stage, wy * M + i, 0)
+                   : frag_rows<KS>(rows_base<KS>(stage, 0, lane), wy * M + i);
+        fx[i] = XT ? frag_cols<TX>(cols_base<TX>(lane), stage + TY * 64, wx * M + i, 0)
+                   : frag_rows<KS>(rows_base<KS>(stage + TY * 64, 0, lane), wx * M + i);
+      }
+#pragma unroll
+      for (int i = 0; i < M; ++i)
+#pragma unroll
+        for (int j = 0; j < M; ++j) acc[i][j] = mfma_bf16(fx[j], fy[i], acc[i][j]);
+      if (s + 1 < steps) fill(lds + ((s + 1) & 1) * STAGE);
+      __syncthreads();
+    }
+    if (MODE == WEIGHTS && a.accumulate && steps == 0) return;
+#pragma unroll
+    for (int i = 0; i < M; ++i)
+#pragma unroll
+      for (int j = 0; j < M; ++j)
+        put<MODE, false, OUT>(a, p, op.width, (wy * M + i) * 16 + (lane & 15), (wx * M + j) * 16 + 4 * (lane >> 4),
+                              acc[i][j]);
+  }
+};
 
+// ---------------------------------------------------------------------------
+// Rows of whole 16-byte chunks go straight to LDS.  TY x TX tiles, WY x WX waves,
+// steps of 128 bytes of z (whole lines; two matrix instructions deep), NS of
+// them in LDS.  A wave holds the fragments of one half step while it reads the
+// next half's, and the loads of step s + NS go out between the matrix
+// instructions of the half in which step s has been read by all: one barrier
+// per step, and no wave stands waiting to issue loads (in one burst they fill
+// the CU's queue, and the wave with them).
+// ---------------------------------------------------------------------------
+template <int MODE, int TY_, int TX_, int WY, int WX, int NS, typename OUT>
+struct Direct {
+  static constexpr int TY = TY_, TX = TX_, KS = 2, NW = WY * WX, THREADS = 64 * NW;
+  static constexpr int MY = TY / WY / 16, MX = TX / WX / 16;
+  static constexpr int IY = TY * KS / 16 / NW, IX = TX * KS / 16 / NW, NI = IY + IX;   // loads of 1 KB per wave and step
+  static constexpr int STEP = 64 * KS, STAGE = (TY + TX) * STEP;
+  // FP4: E8M0 codes of 512 z, 16 bytes per row, two of such in turn
+  static constexpr int SCALES = MODE == FOUR ? (TY + TX) * 16 : 0, IS = SCALES / 256 / NW;
+  static constexpr int LDS = STAGE * NS + 2 * SCALES, PER_SIMD = 2;   // waves, by LDS and registers
+  static constexpr int ZSTEP = (MODE == FOUR ? 128 : 32) * KS;
+  static_assert(TY * KS / 16 % NW == 0 && TX * KS / 16 % NW == 0 && SCALES / 256 % NW == 0, "whole loads per wave");
+  static_assert(MODE != FOUR || NS == 2, "the number of loads of a step varies");
+
+  static __device__ __forceinline__ void dma16_base(uint32_t off, const uint8_t* base, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+                 :: "v"(off), "s"(base), "s"(lds) : "memory", "m0");
+  }
+
+  static __device__ __forceinline__ void run(const TileArgs& a, int64_t b, uint32_t lds) {
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    Place p;
+    if (!find_tile<MODE, TY, TX>(a, b, p)) return;
+    const Operands<MODE> op(a, p);
+    constexpr bool YT = Operands<MODE>::YT, XT = Operands<MODE>::XT;
+    const int steps = (op.zn + ZSTEP - 1) / ZSTEP;
+    const int full = op.zn / ZSTEP;   // steps without an end of z in them
     v4f acc[MY][MX];
 #pragma unroll
     for (int i = 0; i < MY; ++i)
 #pragma unroll
       for (int j = 0; j < MX; ++j) acc[i][j] = (v4f){0.f, 0.f, 0.f, 0.f};
 
-    // the lane's chunks of a step
-    const uint8_t* src[NI];
-    int left[NI];     // values of z (or, transposed, rows of z) from the chunk on to the end of z
-    int wide[NI];     // columns of a transposed chunk inside the tile's extent
+    // the lane's chunks of a step: bytes from the operand's place at that step.
+    // Rows and columns past the extent: any others, never stored.
+    uint32_t off[NI];
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const bool isy = i < IY;
       const int j = wave + NW * (isy ? i : i - IY);
       int row, chunk;
-      if (isy) chunk_of<TY, YT>(j, lane, row, chunk);
-      else chunk_of<TX, XT>(j, lane, row, chunk);
-      const int extent = isy ? p.ny : p.nx, pitch = isy ? ybytes : xbytes;
-      const uint8_t* base = isy ? Y : X;
-      if (isy ? YT : XT) {
-        wide[i] = DIRECT ? 8 : max(0, min(8, extent - chunk * 8));
-        const int c = DIRECT ? min(chunk * 8, extent - 8) : chunk * 8;   // past the end: any column, never stored
-        src[i] = base + (size_t)row * pitch + (DIRECT || wide[i] > 0 ? c * 2 : 0);
-        left[i] = zn - row;
-      } else {
-        wide[i] = 8;
-        src[i] = base + (size_t)min(row, extent - 1) * pitch + chunk * 16;
-        left[i] = zn - chunk * 8;
-      }
+      if (isy) chunk_of<TY, YT, KS>(j, lane, row, chunk);
+      else chunk_of<TX, XT, KS>(j, lane, row, chunk);
+      const int extent = isy ? p.ny : p.nx, pitch = isy ? op.ybytes : op.xbytes;
+      off[i] = (isy ? YT : XT) ? (uint32_t)row * pitch + min(chunk * 16, extent * 2 - 16)
+                               : (uint32_t)min(row, extent - 1) * pitch + chunk * 16;
     }
-    const size_t ystep = YT ? (size_t)ZROWS * ybytes : STEP, xstep = XT ? (size_t)ZROWS * xbytes : STEP;
-
-    // FP4: the E8M0 codes of a step, 4 per row
-    const uint8_t* ssrc[SY + SX + 1];
-    uint32_t sdst[SY + SX + 1];
-    if constexpr (MODE == FOUR) {
-      const int g = a.K / 32;
-#pragma unroll
-      for (int i = 0; i < SY + SX; ++i) {
-        const bool isy = i < SY;
-        const int blocks = (isy ? TY : TX) / 64, blk = (wave + NW * (isy ? i : i - SY)) % blocks;
-        const int row = min(blk * 64 + lane, (isy ? p.ny : p.nx) - 1);
-        ssrc[i] = isy ? a.SY + (size_t)(p.r0 + p.y0 + row) * g : a.SX + ((size_t)p.e * a.N + p.x0 + row) * g;
-        sdst[i] = (TY + TX) * STEP + (isy ? 0 : TY * 4) + blk * 256;
-      }
-    }
-
+    const uint8_t *yp = op.Y, *xp = op.X;   // at the next step to load
+    const size_t ystep = YT ? (size_t)ZSTEP * op.ybytes : STEP, xstep = XT ? (size_t)ZSTEP * op.xbytes : STEP;
     auto place = [&](int i, uint32_t stage) {
       return stage + (i < IY ? (wave + NW * i) * 1024 : TY * STEP + (wave + NW * (i - IY)) * 1024);
     };
-    auto issue = [&](int s, uint32_t stage) {   // DIRECT: the loads of step s
-      const bool whole = s < full;
-#pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const uint8_t* q = src[i];
-        if (!whole && left[i] - 32 * s <= 0) q = reinterpret_cast<const uint8_t*>(&zero_chunk);
-        dma16(q, place(i, stage));
-        src[i] += i < IY ? ystep : xstep;
+    auto load = [&](int i, int s, uint32_t stage, auto whole) {
+      const uint8_t* base = i < IY ? yp : xp;
+      if (decltype(whole)::value || s < full) {
+        dma16_base(off[i], base, place(i, stage));
+      } else {
+        int row, chunk;
+        const int j = wave + NW * (i < IY ? i : i - IY);
+        if (i < IY) chunk_of<TY, YT, KS>(j, lane, row, chunk);
+        else chunk_of<TX, XT, KS>(j, lane, row, chunk);
+        const int z = (i < IY ? YT : XT) ? row : chunk * (MODE == FOUR ? 32 : 8);
+        dma16(s * ZSTEP + z < op.zn ? base + off[i] : reinterpret_cast<const uint8_t*>(&zero_chunk), place(i, stage));
       }
-      if constexpr (MODE == FOUR) {
+    };
+    auto advance = [&]() {
+      yp += ystep;
+      xp += xstep;
+    };
+    // FP4: the codes of steps s and s + 1, 4 lanes per row
+    auto load_scales = [&](int s) {
+      const int g = a.K / 32, word = 2 * s + (lane & 3);   // of 128 z
 #pragma unroll
-        for (int i = 0; i < SY + SX; ++i) {
-          vm_dma4(ssrc[i], stage + sdst[i]);
-          ssrc[i] += 4;
-        }
+      for (int i = 0; i < IS; ++i) {
+        const int j = wave * IS + i, row = j * 16 + (lane >> 2);   // TY % 16 == 0: a load is of one operand
+        const bool isy = j * 16 < TY;
+        const uint8_t* q = isy ? a.SY + (size_t)(p.r0 + p.y0 + min(row, p.ny - 1)) * g
+                               : a.SX + ((size_t)p.e * a.N + p.x0 + min(row - TY, p.nx - 1)) * g;
+        vm_dma4(word * 128 < op.zn ? q + word * 4 : reinterpret_cast<const uint8_t*>(&zero_chunk),
+                lds + STAGE * NS + ((s >> 1) & 1) * SCALES + j * 256);
       }
     };
 
     const int wy = wave / WX, wx = wave % WX;
-    auto compute = [&](uint32_t stage) {
-      v4i fy[MY], fx[MX];
+    const int nb = ((p.ny + 15) / 16 - wy + WY - 1) / WY;   // the wave's row blocks: wy, wy + WY, ...
+    v4i fy[4], fx[2][MX];
+    uint32_t ey[MY], ex[MX];
+    // addresses at stage 0: by half where z is contiguous
+    const uint32_t y0 = lds + wy * 16 * STEP, x0 = lds + TY * STEP + wx * MX * 16 * STEP;
+    const uint32_t ya[2] = {YT ? cols_base<TY>(lane) : rows_base<KS>(y0, 0, lane), YT ? 0 : rows_base<KS>(y0, 1, lane)};
+    const uint32_t xa[2] = {XT ? cols_base<TX>(lane) : rows_base<KS>(x0, 0, lane), XT ? 0 : rows_base<KS>(x0, 1, lane)};
+    auto read_y = [&](int h, int i, uint32_t stage) {
+      fy[i & 3] = YT ? frag_cols<TY>(ya[0], lds + stage, i * WY + wy, h) : frag_rows<KS>(ya[h] + stage, i * WY);
+    };
+    auto read_x = [&](int h, int j, uint32_t stage) {
+      fx[h][j] = XT ? frag_cols<TX>(xa[0], lds + stage + TY * STEP, wx * MX + j, h) : frag_rows<KS>(xa[h] + stage, j);
+    };
+    // The codes of the lane's blocks for the next 512 z, byte t of the t-th 128
+    auto scales = [&](int s) {
+      const uint32_t at = lds + STAGE * NS + ((s >> 1) & 1) * SCALES + (lane & 15) * 16;
+      const uint32_t q = lane >> 4, sel = q | ((4 + q) << 8);
+      auto word = [&](uint32_t row) {
+        const v4i w = *(lds_v4i*)(uintptr_t)(at + row * 16);
+        const uint32_t lo = __builtin_amdgcn_perm(w[1], w[0], sel), hi = __builtin_amdgcn_perm(w[3], w[2], sel);
+        return __builtin_amdgcn_perm(hi, lo, 0x05040100u);
+      };
 #pragma unroll
-      for (int i = 0; i < MY; ++i)
-        fy[i] = YT ? frag_cols<TY>(stage, wy * MY + i, lane) : frag_rows(stage, wy * MY + i, lane);
+      for (int i = 0; i < MY; ++i) ey[i] = word((i * WY + wy) * 16);
 #pragma unroll
-      for (int j = 0; j < MX; ++j)
-        fx[j] = XT ? frag_cols<TX>(stage + TY * STEP, wx * MX + j, lane) : frag_rows(stage + TY * STEP, wx * MX + j, lane);
+      for (int j = 0; j < MX; ++j) ex[j] = word(TY + (wx * MX + j) * 16);
+    };
+    auto multiply = [&](int h, int i) {   // row block i with half h
+#pragma unroll
+      for (int j = 0; j < MX; ++j) {
+        if constexpr (MODE == FOUR) {
+          const v8i x8 = {fx[h][j][0], fx[h][j][1], fx[h][j][2], fx[h][j][3], 0, 0, 0, 0};
+          const v8i y8 = {fy[i & 3][0], fy[i & 3][1], fy[i & 3][2], fy[i & 3][3], 0, 0, 0, 0};
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x8, y8, acc[i][j], 4, 4, 0, (int)ex[j], 0, (int)ey[i]);
+        } else {
+          acc[i][j] = mfma_bf16(fx[h][j], fy[i & 3], acc[i][j]);
+        }
+      }
+    };
+    auto next_scales = [&]() {
       if constexpr (MODE == FOUR) {
-        int ey[MY], ex[MX];
-        const uint32_t sc = stage + (TY + TX) * STEP + (lane & 15) * 4 + (lane >> 4);
 #pragma unroll
-        for (int i = 0; i < MY; ++i) ey[i] = *(lds_u8*)(uintptr_t)(sc + (wy * MY + i) * 64);
+        for (int i = 0; i < MY; ++i) ey[i] >>= 8;
 #pragma unroll
-        for (int j = 0; j < MX; ++j) ex[j] = *(lds_u8*)(uintptr_t)(sc + TY * 4 + (wx * MX + j) * 64);
-#pragma unroll
-        for (int i = 0; i < MY; ++i)
-#pragma unroll
-          for (int j = 0; j < MX; ++j) {
-            const v8i x8 = {fx[j][0], fx[j][1], fx[j][2], fx[j][3], 0, 0, 0, 0};
-            const v8i y8 = {fy[i][0], fy[i][1], fy[i][2], fy[i][3], 0, 0, 0, 0};
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x8, y8, acc[i][j], 4, 4, 0, ex[j], 0, ey[i]);
-          }
-      } else {
-#pragma unroll
-        for (int i = 0; i < MY; ++i)
-#pragma unroll
-          for (int j = 0; j < MX; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, fx[j]),
-                                                                __builtin_bit_cast(v8bf, fy[i]), acc[i][j], 0, 0, 0);
+        for (int j = 0; j < MX; ++j) ex[j] >>= 8;
       }
     };
 
-    if constexpr (DIRECT) {
+    // Step s: groups g = 0 .. 2 MY - 1 of MX matrix instructions, one row block of
+    // one half each.  Reads run AHEAD groups before their use; the loads of step
+    // s + NS - 1 go out with the first groups (their place was read in step s -
+    // 1); before the last AHEAD groups all waves have read step s and step s + 1
+    // has landed.  WHOLE: the steps up to s + NS - 1 have all of their z; ALL: the
+    // wave has all of its row blocks.
+    constexpr int GROUPS = KS * MY, AHEAD = 2, EACH = std::max(2, (NI + GROUPS - AHEAD - 1) / (GROUPS - AHEAD));
+    static_assert(MY >= 4, "four row blocks are held at a time");
+    uint32_t stage = 0, spare = (NS - 1) * STAGE;
+    auto step = [&](int s, auto whole_, auto all_) {
+      constexpr bool WHOLE = decltype(whole_)::value, ALL = decltype(all_)::value;
+      const bool two = WHOLE || s * ZSTEP + ZSTEP / 2 < op.zn;   // the second half has z
+      const bool more = WHOLE || s + NS - 1 < steps, last = !WHOLE && s + 1 >= steps;
+      const uint32_t after = stage == (NS - 1) * STAGE ? 0 : stage + STAGE;
+      if (MODE == FOUR && !(s & 1)) scales(s);
 #pragma unroll
-      for (int s = 0; s < NS - 1; ++s)
-        if (s < steps) issue(s, lds + s * STAGE);
-      uint32_t slot = 0, next = (NS - 1) * STAGE;
-      for (int s = 0; s < steps; ++s) {
-        // step s landed: the NS - 2 issued after it may still be under way
-        if (s + NS - 2 < steps) wait_and_meet<(NS - 2) * PER>();
-        else wait_and_meet<0>();
-        if (s + NS - 1 < steps) issue(s + NS - 1, lds + next);   // where step s - 1 was
-        compute(lds + slot);
-        slot = slot == (NS - 1) * STAGE ? 0 : slot + STAGE;
-        next = next == (NS - 1) * STAGE ? 0 : next + STAGE;
-      }
-    } else {
-      v4i reg[NI];
-      auto fetch = [&](int s) {
+      for (int g = 0; g < GROUPS; ++g) {
+        const int h = g / MY, i = g % MY;
+        if (g == GROUPS - AHEAD) {
+          if (!last) {
+            if (WHOLE || s + NS - 1 < steps) wait_and_meet<(NS - 2) * NI>();
+            else wait_and_meet<0>();
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-          const bool tr = i < IY ? YT : XT;
-          const int z = left[i] - 32 * s;
-          reg[i] = load_any(src[i], z <= 0 ? 0 : tr ? wide[i] : z);
-          src[i] += i < IY ? ystep : xstep;
+            for (int j = 0; j < MX; ++j) read_x(0, j, after);
+          }
         }
-      };
-      auto put = [&](uint32_t stage) {
+        if (g + AHEAD < GROUPS) {
+          if (g + AHEAD < MY || two) read_y((g + AHEAD) / MY, (g + AHEAD) % MY, stage);
+        } else if (!last) {
+          read_y(0, g + AHEAD - GROUPS, after);
+        }
+        if (g < MY && two) {
 #pragma unroll
-        for (int i = 0; i < NI; ++i) *(lds_v4i*)(uintptr_t)(place(i, stage) + lane * 16) = reg[i];
-      };
-      if (steps > 0) {
-        fetch(0);
-        put(lds);
-        __syncthreads();
+          for (int j = 0; j < MX; ++j)
+            if (j * (MY - 1) / MX == g) read_x(1, j, stage);   // spread over the first half
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if ((ALL || i < nb) && (h == 0 || two)) multiply(h, i);
+        __builtin_amdgcn_sched_barrier(0);
+        if (more && g * EACH < NI) {
+#pragma unroll
+          for (int l = g * EACH; l < (g + 1) * EACH && l < NI; ++l) load(l, s + NS - 1, lds + spare, whole_);
+          if (MODE == FOUR && (g + 1) * EACH >= NI && (s & 1)) load_scales(s + 1);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        if (g == MY - 1 || g == GROUPS - 1) next_scales();
       }
-      for (int s = 0; s < steps; ++s) {
-        if (s + 1 < steps) fetch(s + 1);
-        compute(lds + (s & 1) * STAGE);
-        if (s + 1 < steps) put(lds + ((s + 1) & 1) * STAGE);
-        __syncthreads();
+      if (more) advance();
+      stage = after;
+      spare = spare == (NS - 1) * STAGE ? 0 : spare + STAGE;
+    };
+
+#pragma unroll
+    for (int s = 0; s < NS - 1; ++s) {
+      if (s < steps) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) load(i, s, lds + s * STAGE, std::false_type());
+        advance();
       }
     }
+    if (MODE == FOUR) load_scales(0);
+    if (MODE != FOUR && steps >= NS - 1) wait_and_meet<(NS - 2) * NI>();
+    else wait_and_meet<0>();
+    if (steps > 0) {
+#pragma unroll
+      for (int j = 0; j < MX; ++j) read_x(0, j, 0);
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) read_y(0, i, 0);
+    }
+    int s = 0;
+    if (nb == MY)
+      for (; s + NS - 1 < full; ++s) step(s, std::true_type(), std::true_type());
+    else
+      for (; s + NS - 1 < full; ++s) step(s, std::true_type(), std::false_type());
+    for (; s < steps; ++s) step(s, std::false_type(), std::false_type());
 
     if (MODE == WEIGHTS && a.accumulate && steps == 0) return;
-    const int width = MODE == ROWS || MODE == WEIGHTS ? a.K : a.N;
-    OUT* out = static_cast<OUT*>(a.out) +
-               (MODE == WEIGHTS ? (size_t)p.e * a.N + p.y0 : (size_t)(p.r0 + p.y0)) * width + p.x0;
 #pragma unroll
-    for (int i = 0; i < MY; ++i) {
-      const int y = (wy * MY + i) * 16 + (lane & 15);
+    for (int i = 0; i < MY; ++i)
 #pragma unroll
-      for (int j = 0; j < MX; ++j) {
-        const int x = (wx * MX + j) * 16 + 4 * (lane >> 4);
-        if (y >= p.ny || x >= p.nx) continue;
-        OUT* o = out + (size_t)y * width + x;
-        v4f v = acc[i][j];
-        const int n = DIRECT ? 4 : min(4, p.nx - x);
-        if (MODE == WEIGHTS && a.accumulate) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (c < n) v[c] += sizeof(OUT) == 4 ? (float)o[c] : __uint_as_float((uint32_t)(uint16_t)o[c] << 16);
-        }
-        if constexpr (sizeof(OUT) == 4) {
-          if (DIRECT) *reinterpret_cast<v4f*>(o) = v;
-          else
-            for (int c = 0; c < n; ++c) o[c] = v[c];
-        } else {
-          if (DIRECT) store_bf16x4(o, v);
-          else
-            for (int c = 0; c < n; ++c) o[c] = __builtin_bit_cast(uint16_t, (__bf16)v[c]);
-        }
-      }
-    }
+      for (int j = 0; j < MX; ++j)
+        put<MODE, true, OUT>(a, p, op.width, (i * WY + wy) * 16 + (lane & 15), (wx * MX + j) * 16 + 4 * (lane >> 4),
+                             acc[i][j]);
   }
 };
 
-template <int MODE, int TY, int TX, int WY, int WX, int NS, bool DIRECT, typename OUT>
-__global__ void __launch_bounds__(64 * WY * WX, 2)
+template <typename T>
+__global__ void __launch_bounds__(T::THREADS, T::PER_SIMD)
 tile_kernel(TileArgs a, int64_t b0) {
-  Tile<MODE, TY, TX, WY, WX, NS, DIRECT, OUT>::run(a, b0 + blockIdx.x);
+  extern __shared__ __align__(1024) uint8_t smem[];
+  T::run(a, b0 + blockIdx.x, lds_u32(smem));
 }
 
-template <int MODE, int TY, int TX, int WY, int WX, int NS, bool DIRECT, typename OUT>
+template <int MODE, typename T>
 hipError_t launch(const TileArgs& a, hipStream_t stream) {
-  using T = Tile<MODE, TY, TX, WY, WX, NS, DIRECT, OUT>;
-  const auto kernel = &tile_kernel<MODE, TY, TX, WY, WX, NS, DIRECT, OUT>;
   if (T::LDS > 64 * 1024) {
     // more than a launch has without asking; once per device
     static std::atomic<uint64_t> allowed{0};
@@ -400,29 +580,47 @@ hipError_t launch(const TileArgs& a, hipStream_t stream) {
     if (e != hipSuccess) return e;
     const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
     if (!(allowed.load(std::memory_order_acquire) & bit)) {
-      e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, T::LDS);
+      e = hipFuncSetAttribute(reinterpret_cast<const void*>(&tile_kernel<T>), hipFuncAttributeMaxDynamicSharedMemorySize,
+                              T::LDS);
       if (e != hipSuccess) return e;
       allowed.fetch_or(bit, std::memory_order_release);
     }
   }
   // tiles: known for the weights, otherwise at most (each expert's last may be
   // part of one); workgroups come in eights, one per XCD
-  const int64_t width = MODE == ROWS || MODE == WEIGHTS ? a.K : a.N, nt = (width + TX - 1) / TX;
-  const int64_t rows = MODE == WEIGHTS ? (int64_t)a.E * ((a.N + TY - 1) / TY)
-                                       : (a.R + (int64_t)std::min(a.E, a.R) * (TY - 1)) / TY;
-  return in_launches((rows * nt + 7) / 8 * 8, T::THREADS, [&](int64_t b, int64_t n) {
-    hipLaunchKernelGGL((tile_kernel<MODE, TY, TX, WY, WX, NS, DIRECT, OUT>), dim3((unsigned)n), dim3(T::THREADS), T::LDS,
-                       stream, a, b);
+  const int64_t width = MODE == ROWS || MODE == WEIGHTS ? a.K : a.N, nt = (width + T::TX - 1) / T::TX;
+  const int64_t eights = MODE == WEIGHTS ? a.E * (((a.N + T::TY - 1) / T::TY * nt + 7) / 8)
+                                         : ((a.R + (int64_t)std::min(a.E, a.R) * (T::TY - 1)) / T::TY * nt + 7) / 8;
+  return in_launches(eights * 8, T::THREADS, [&](int64_t b, int64_t n) {
+    hipLaunchKernelGGL(tile_kernel<T>, dim3((unsigned)n), dim3(T::THREADS), T::LDS, stream, a, b);
   });
 }
 
 bool chunks16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
+// Tiles by the mean number of rows of an expert (all that the host knows).
+// 4096 x 6144, 32 experts, unevenly filled, us a call, forward | row gradient:
+//   rows        16          64          128         288          512          1024
+//   64 x 128    273 | 279   368 | 365   479 | 471   824 | 787    1344 | 1285  2545 | 2437
+//   128 x 256   273 | 263   342 | 322   416 | 384   601 | 586     925 | 901   1688 | 1666
+//   256 x 256   340 | 319   367 | 342   496 | 439   667 | 646     975 | 888   1639 | 1581
+// Where tiles are few, the small ones fill the chip (forward, 12 experts of 43
+// rows, 6144 x 3584: 113 against 129 us); the row gradient reads whole lines of
+// the weights only with 256 columns (127 against 103).  The weights' gradient has
+// its largest tiles at any number of rows (16: 671 against 750 us with 128 x 256,
+// 288: 1133 / 1253, 1024: 2070 / 2282).
 template <int MODE, typename OUT>
 hipError_t launch_bf16(const TileArgs& a, hipStream_t stream) {
-  if (a.N % 8 || a.K % 8 || !chunks16(a.Y) || !chunks16(a.X) || !chunks16(a.out))
-    return launch<MODE, 128, 128, 2, 2, 2, false, OUT>(a, stream);
-  return launch<MODE, 128, 256, 2, 2, 3, true, OUT>(a, stream);
+  // A tile's offsets within an operand are 32 bits: 256 rows, or 64 of z, of 8 MB
+  // at most.
+  if (a.N % 8 || a.K % 8 || !chunks16(a.Y) || !chunks16(a.X) || !chunks16(a.out) || a.N > (1 << 22))
+    return launch<MODE, General<MODE, OUT>>(a, stream);
+  const int rows = a.R / a.E;
+  if constexpr (MODE == FWD)
+    if (rows <= 48) return launch<MODE, Direct<MODE, 64, 128, 1, 4, 3, OUT>>(a, stream);
+  if constexpr (MODE != WEIGHTS)
+    if (rows <= 768) return launch<MODE, Direct<MODE, 128, 256, 2, 4, 3, OUT>>(a, stream);
+  return launch<MODE, Direct<MODE, 256, 256, 2, 4, 2, OUT>>(a, stream);
 }
 
 }  // namespace
@@ -433,7 +631,12 @@ hipError_t launch_grouped_wgrad(const TileArgs& a, bool f32, hipStream_t stream)
   return f32 ? launch_bf16<WEIGHTS, float>(a, stream) : launch_bf16<WEIGHTS, uint16_t>(a, stream);
 }
 hipError_t launch_grouped_a4(const TileArgs& a, hipStream_t stream) {
-  return launch<FOUR, 128, 256, 2, 2, 3, true, uint16_t>(a, stream);
+  // as above; 16 rows: 84, 88 and 108 us with these three, 64: 134, 125 and 125,
+  // 128: 186, 159 and 170, 288: 311, 243 and 239, 1024: 882, 671 and 576
+  const int rows = a.R / a.E;
+  if (rows <= 32) return launch<FOUR, Direct<FOUR, 64, 128, 1, 4, 2, uint16_t>>(a, stream);
+  if (rows <= 200) return launch<FOUR, Direct<FOUR, 128, 128, 2, 2, 2, uint16_t>>(a, stream);
+  return launch<FOUR, Direct<FOUR, 256, 256, 2, 4, 2, uint16_t>>(a, stream);
 }
 
 }  // namespace w4a8

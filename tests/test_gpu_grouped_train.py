@@ -42,6 +42,7 @@ def _check(got, want, mag, Z, half=2.0 ** -8):
 CASES = [
     ([1], 8, 8), ([5, 0, 3], 16, 8), ([0, 0, 7], 40, 24), ([64, 1, 63, 65], 128, 96), ([130, 0, 257, 31, 2], 264, 72),
     ([16] * 12, 256, 512), ([128, 127, 129], 520, 136), ([300, 900], 384, 1024), ([3, 1, 4, 1, 5] * 30, 64, 64),
+    ([1700, 0, 900], 264, 200), ([2000], 520, 328), ([801, 815], 72, 456),
     # not whole 16-byte pieces
     ([1], 1, 1), ([3, 0, 5], 7, 5), ([40, 33], 33, 31), ([129, 1], 130, 257), ([20, 200], 255, 64), ([65], 64, 129),
     ([1] * 100, 12, 10),
@@ -185,6 +186,22 @@ def test_empty_and_refusals(gpu_lib):
                  lambda: gpu_lib.grouped_gemm_wgrad(A, A, z, out=torch.empty((2, 16, 16), dtype=torch.float16, device="cuda"))):
         with pytest.raises(TypeError):
             call()
+
+
+def test_wide_weights(gpu_lib):
+    """More columns than a tile's 32-bit offsets span."""
+    N, K = (1 << 22) + 8, 8
+    off = _off([2, 3])
+    A, W = _draw(1, 5, K)[0], torch.zeros((2, N, K), dtype=torch.bfloat16, device="cuda")
+    W[1, -3:] = 1.0
+    C = gpu_lib.grouped_gemm_bf16(_dev(A), W, off)
+    want = bf16_bits_to_f64(A)[2:].sum(axis=1)
+    assert np.allclose(C[2:, -3:].double().cpu().numpy(), want[:, None], rtol=2.0 ** -7, atol=2.0 ** -7)
+    assert (C[:, :-3] == 0).all() and (C[:2] == 0).all()
+    dA = gpu_lib.grouped_gemm_dgrad(torch.ones_like(C), W, off)
+    assert (dA[2:] == 3.0).all() and (dA[:2] == 0).all()
+    dW = gpu_lib.grouped_gemm_wgrad(C, _dev(A), off, out=W)
+    assert (dW[0] == 0).all() and (dW[1, :-3] == 0).all() and (dW[1, -3:] != 0).any()
 
 
 def test_offsets_past_32_bits(gpu_lib):
