@@ -31,6 +31,7 @@ typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 constexpr float kScaleFloor = 7.888609052210118e-31f;  // 2^-100
 constexpr int NORM_WAVES = 16;       // most waves of a workgroup
 constexpr int NORM_CHUNKS = 4;       // most chunks of 8 columns that a thread holds
+constexpr int GRAD_WAVES = 8;        // of the gradient, whose threads hold three rows' chunks and dw
 
 // 8 bf16 columns of a row.  VEC: 16-byte aligned and whole.  Otherwise a chunk
 // may start at any 2 bytes and its last n < 8 columns are read one by one (what
@@ -304,7 +305,7 @@ rms_norm_long_kernel(NormArgs a, int64_t row0) {
 // The gradient: workgroup b takes rows b, b + gridDim.x, ... and keeps its part
 // of dw in registers, written to partials[b][K] at the end.
 template <int NCH, bool VEC>
-__global__ void __launch_bounds__(64 * NORM_WAVES)
+__global__ void __launch_bounds__(64 * GRAD_WAVES)
 rms_norm_backward_kernel(NormGradArgs a) {
   __shared__ double sums[2][2][NORM_WAVES];
   const int waves = blockDim.x >> 6;
@@ -428,19 +429,22 @@ rms_norm_backward_long_kernel(NormGradArgs a) {
   }
 }
 
-// dw[k] = sum over the workgroups' parts, 64 columns and 16 runs of parts per
+// dw[k] = sum over the workgroups' parts, 32 columns and 32 runs of parts per
 // workgroup, in 64 bits and a fixed order.
 __global__ void __launch_bounds__(1024)
 norm_weight_sum_kernel(const float* __restrict__ partials, int parts, int K, float* __restrict__ dw) {
-  __shared__ double s[16][64];
-  const int k = blockIdx.x * 64 + (threadIdx.x & 63), run = threadIdx.x >> 6;
+  __shared__ double s[32][33];
+  const int c = threadIdx.x & 31, k = blockIdx.x * 32 + c, run = threadIdx.x >> 5;
   double v = 0.0;
-  if (k < K)
-    for (int p = run; p < parts; p += 16) v += (double)partials[(size_t)p * K + k];
-  s[run][threadIdx.x & 63] = v;
+  if (k < K) {
+    const float* p = partials + (size_t)run * K + k;
+#pragma unroll 8
+    for (int i = run; i < parts; i += 32, p += (size_t)32 * K) v += (double)*p;
+  }
+  s[run][c] = v;
   __syncthreads();
   if (run == 0 && k < K) {
-    for (int i = 1; i < 16; ++i) v += s[i][threadIdx.x];
+    for (int i = 1; i < 32; ++i) v += s[i][c];
     dw[k] = (float)v;
   }
 }
@@ -482,23 +486,26 @@ hipError_t launch_rms_norm_backward(const NormGradArgs& a, hipStream_t stream) {
   const int chunks = (a.K + 7) / 8, parts = norm_backward_parts(a.T);
   const bool vec = a.K % 8 == 0 && vec_ok(a.h) && vec_ok(a.dy) && vec_ok(a.dres) && vec_ok(a.dx) && vec_ok(a.w);
   if (parts > 0) {
-    const int nch = chunks <= 256 ? 1 : 2, most = 64 * NORM_WAVES;
+    const int most = 64 * GRAD_WAVES;
+    int nch = chunks <= 256 ? 1 : 2;
+    if (chunks > most * nch) nch = 4;
     const int threads = std::min(most, ((chunks + nch - 1) / nch + 63) / 64 * 64);
     const dim3 grid(parts), blk(threads);
 #define W4A8_NORM(N)                                                                        \
   if (vec) hipLaunchKernelGGL((rms_norm_backward_kernel<N, true>), grid, blk, 0, stream, a); \
   else hipLaunchKernelGGL((rms_norm_backward_kernel<N, false>), grid, blk, 0, stream, a)
-    if (chunks > most * 2) {   // of 3 streams: half the forward pass's chunks fit
-      if (vec) hipLaunchKernelGGL(rms_norm_backward_long_kernel<true>, grid, blk, 0, stream, a);
-      else hipLaunchKernelGGL(rms_norm_backward_long_kernel<false>, grid, blk, 0, stream, a);
+    if (chunks > most * NORM_CHUNKS) {
+      if (vec) hipLaunchKernelGGL(rms_norm_backward_long_kernel<true>, grid, dim3(64 * NORM_WAVES), 0, stream, a);
+      else hipLaunchKernelGGL(rms_norm_backward_long_kernel<false>, grid, dim3(64 * NORM_WAVES), 0, stream, a);
     } else if (nch == 1) { W4A8_NORM(1); }
-    else { W4A8_NORM(2); }
+    else if (nch == 2) { W4A8_NORM(2); }
+    else { W4A8_NORM(4); }
 #undef W4A8_NORM
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   if (a.dw)
-    hipLaunchKernelGGL(norm_weight_sum_kernel, dim3((a.K + 63) / 64), dim3(1024), 0, stream, a.partials, parts, a.K, a.dw);
+    hipLaunchKernelGGL(norm_weight_sum_kernel, dim3((a.K + 31) / 32), dim3(1024), 0, stream, a.partials, parts, a.K, a.dw);
   return hipGetLastError();
 }
 

@@ -120,7 +120,7 @@ struct NormGradArgs {
   int T, K, w_f32;
   float eps;
 };
-constexpr int NORM_PARTS = 1024;   // most workgroups of the gradient, each with a part of dw
+constexpr int NORM_PARTS = 512;   // most workgroups of the gradient, each with a part of dw
 int norm_backward_parts(int T);
 hipError_t launch_rms_norm(const NormArgs& args, hipStream_t stream);
 hipError_t launch_rms_norm_backward(const NormGradArgs& args, hipStream_t stream);
