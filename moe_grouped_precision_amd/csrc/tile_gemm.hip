@@ -100,6 +100,7 @@ __device__ __forceinline__ v4i frag_cols(uint32_t base, uint32_t tile, int blk, 
 struct Place {
   int e, y0, ny, x0, nx;    // expert, tile
   int r0, rows;             // the expert's rows
+  int odd;                  // the tiles as a chessboard
 };
 
 // The tile of workgroup b, false if it has none or the offsets are not those of
@@ -167,6 +168,7 @@ __device__ __forceinline__ bool find_tile(const TileArgs& a, int64_t b, Place& p
     p.y0 = uniform(yt * per);
     p.ny = uniform(min(per, p.rows - p.y0));
   }
+  p.odd = uniform((yt ^ xt) & 1);
   p.x0 = uniform(xt) * TX;
   p.nx = min(TX, width - p.x0);
   return true;
@@ -410,10 +412,15 @@ struct Direct {
         dma16(s * ZSTEP + z < op.zn ? base + off[i] : reinterpret_cast<const uint8_t*>(&zero_chunk), place(i, stage));
       }
     };
-    auto advance = [&]() {
-      yp += ystep;
-      xp += xstep;
+    // Every second tile takes the whole steps of a pair the other way round, so that
+    // neighbours in step ask for different lines (2% on every product).
+    auto z_of = [&](int s) { return (s | 1) < full ? s ^ p.odd : s; };
+    auto advance = [&](int s) {
+      const int z = z_of(s);
+      yp = op.Y + (size_t)z * ystep;
+      xp = op.X + (size_t)z * xstep;
     };
+    advance(0);
     // FP4: the codes of steps s and s + 1, 4 lanes per row
     auto load_scales = [&](int s) {
       const int g = a.K / 32, word = 2 * s + (lane & 3);   // of 128 z
@@ -449,7 +456,7 @@ struct Direct {
       auto word = [&](uint32_t row) {
         const v4i w = *(lds_v4i*)(uintptr_t)(at + row * 16);
         const uint32_t lo = __builtin_amdgcn_perm(w[1], w[0], sel), hi = __builtin_amdgcn_perm(w[3], w[2], sel);
-        return __builtin_amdgcn_perm(hi, lo, 0x05040100u);
+        return __builtin_amdgcn_perm(hi, lo, z_of(s) == s ? 0x05040100u : 0x01000504u);
       };
 #pragma unroll
       for (int i = 0; i < MY; ++i) ey[i] = word((i * WY + wy) * 16);
@@ -524,7 +531,7 @@ struct Direct {
         }
         if (g == MY - 1 || g == GROUPS - 1) next_scales();
       }
-      if (more) advance();
+      if (more) advance(s + NS);
       stage = after;
       spare = spare == (NS - 1) * STAGE ? 0 : spare + STAGE;
     };
@@ -534,7 +541,7 @@ struct Direct {
       if (s < steps) {
 #pragma unroll
         for (int i = 0; i < NI; ++i) load(i, s, lds + s * STAGE, std::false_type());
-        advance();
+        advance(s + 1);
       }
     }
     if (MODE == FOUR) load_scales(0);
