@@ -4,9 +4,8 @@
 
 Training: gate -> route prep -> dispatch -> grouped product -> SwiGLU (its
 input kept in 8 bits) -> grouped product -> combine, and back: the gradients
-of combine, SwiGLU, dispatch and gate.  The library multiplies by the experts
-in the forward direction; the gradient through a frozen expert is a plain
-product with its decoded weights here.
+of combine, SwiGLU, dispatch and gate.  The gradient through the frozen
+experts is the grouped row gradient with their decoded weights.
 
 Decoding: a few tokens run through the same experts without any grouping, by
 matrix-vector products.
@@ -68,18 +67,11 @@ class MoEBlock:
         x, logits, ids, weights, offsets, rows, codes, scales, c2 = self.saved
         k = self.top_k
         dc2, dweights = w4a8.combine_backward(c2, dout, rows, weights, k)
-        bounds = offsets.tolist()
-        dh = torch.zeros((dc2.shape[0], self.I), dtype=torch.bfloat16, device=x.device)
-        da = torch.zeros((dc2.shape[0], self.H), dtype=torch.bfloat16, device=x.device)
-        for e in range(self.E):
-            lo, hi = bounds[e], bounds[e + 1]
-            if hi > lo:
-                dh[lo:hi] = dc2[lo:hi] @ decode_mxfp4(self.B2[e], self.SB2[e])
+        w2 = w4a8.dequantize_fp4(self.B2, self.SB2, w4a8.WSCALE_MX)
+        dh = w4a8.grouped_gemm_dgrad(dc2, w2, offsets)
         dc1 = w4a8.swiglu_backward(codes, scales, dh)
-        for e in range(self.E):
-            lo, hi = bounds[e], bounds[e + 1]
-            if hi > lo:
-                da[lo:hi] = dc1[lo:hi] @ decode_mxfp4(self.B13[e], self.SB13[e])
+        w13 = w4a8.dequantize_fp4(self.B13, self.SB13, w4a8.WSCALE_MX)
+        da = w4a8.grouped_gemm_dgrad(dc1, w13, offsets)
         dlogits = w4a8.topk_gate_backward(logits, ids, dweights)
         dx = w4a8.dispatch_backward(da, rows, k)
         return (dx.float() + dlogits @ self.router).to(torch.bfloat16), dlogits.t() @ x.float()

@@ -578,8 +578,8 @@ int w4a8_swiglu_backward(const uint8_t* ckpt_fp8_dev, const float* ckpt_scales_d
  * A_fp8_dev, a_scales_dev, a_scale_layout: out uint8 [T][K] codes and fp32
  *                    scales in the layouts of w4a8_grouped_gemm (R = T), or both NULL.
  * At least one of y and A is asked for.  y and sum may be the buffers of x or
- * of the residual (not y and sum the same one); otherwise no output overlaps
- * an input or another output.
+ * of the residual, never the same one (W4A8_ERR_SHAPE); otherwise no output
+ * overlaps an input or another output.
  * Sums are taken in 64 bits and any finite row has its value (no overflow of
  * the squares).  Rows of zeros with eps = 0, and rows with an infinity or a
  * NaN, are what the formula gives (NaN, or 0 beside an infinity); a group of

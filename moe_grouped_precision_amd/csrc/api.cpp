@@ -670,6 +670,7 @@ int w4a8_rms_norm(const uint16_t* x_bf16_dev, const uint16_t* residual_bf16_dev,
     return fail(W4A8_ERR_LAYOUT, "a_scale_layout=%d is neither row-major (0) nor M-major (1)", a_scale_layout);
   if (!A_fp8_dev != !a_scales_dev) return fail(W4A8_ERR_NULL, "8-bit codes and scales go together");
   if (T > 0 && (!x_bf16_dev || (!y_bf16_dev && !A_fp8_dev))) return fail(W4A8_ERR_NULL, "null pointer argument");
+  if (y_bf16_dev && y_bf16_dev == sum_bf16_dev) return fail(W4A8_ERR_SHAPE, "y and sum are the same buffer");
   if (!aligned(x_bf16_dev, 2) || !aligned(residual_bf16_dev, 2) || !aligned(y_bf16_dev, 2) ||
       !aligned(sum_bf16_dev, 2) || !aligned(A_fp8_dev, 16) || !aligned(a_scales_dev, 4))
     return fail(W4A8_ERR_ALIGN, "x, residual, y and sum need 2-byte, A 16-byte, scales 4-byte alignment");

@@ -37,7 +37,8 @@ def _caller(f, ok):
 
 
 def test_rms_norm(lib):
-    c = _caller(lib.w4a8_rms_norm, (P, P, P, 1, 4, 256, 1e-6, P, P, P, P, 0, NUL))
+    c = _caller(lib.w4a8_rms_norm, (P, P, P, 1, 4, 256, 1e-6, P, Q, P, P, 0, NUL))
+    assert c(a8=P) == SHAPE                                           # y and sum the same buffer
     assert c(a4=-1) == SHAPE and c(a5=0) == SHAPE and c(a5=(1 << 20) + 1) == SHAPE
     assert c(a5=200) == SHAPE                                         # codes need whole groups
     assert c(a6=-1e-9) == SHAPE and c(a6=float("nan")) == SHAPE
