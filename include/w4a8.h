@@ -634,21 +634,29 @@ size_t w4a8_rms_norm_backward_bytes(int T, int K);
  * dW_dev, dW_type     out [E][N][K] of W4A8_TYPE_F32 or W4A8_TYPE_BF16; zeros
  *                     for experts without rows.  accumulate != 0 adds the sum
  *                     to what dW holds (in fp32, one rounding).
- * Every run gives the same bits.  No output overlaps an input.
+ * workspace_dev       w4a8_grouped_gemm_workspace_bytes(...) bytes, 16-byte aligned,
+ *                     not shared by calls that may run at a time: products of
+ *                     few tiles and a long sum then take it in slices, all
+ *                     over the chip.  NULL: in one piece.
+ * Every run gives the same bits (with and without a workspace the sums have
+ * another order).  No output overlaps an input.
  * Limits: 1 <= E <= W4A8_MAX_EXPERTS, R >= 0, 1 <= N <= W4A8_MAX_N, 1 <= K <=
  * W4A8_MAX_K.  R == 0: nothing to do, except that wgrad writes its zeros.
- * bf16 buffers need 2-byte, fp32 ones 4-byte alignment; with N % 8 == 0, K % 8
- * == 0 and 16-byte alignment of all three the rows go to LDS as whole 16-byte
- * pieces, otherwise through registers.
+ * bf16 buffers need 2-byte, fp32 ones 4-byte alignment; with inputs at 16-byte
+ * alignment, K % 8 == 0 and, for the gradients, N % 8 == 0 the rows go to LDS as
+ * whole 16-byte pieces, otherwise through registers.
  */
+enum { W4A8_PRODUCT_BF16 = 0, W4A8_PRODUCT_DGRAD = 1, W4A8_PRODUCT_WGRAD = 2, W4A8_PRODUCT_A4 = 3 };
+size_t w4a8_grouped_gemm_workspace_bytes(int product, int R, int E, int N, int K);
 int w4a8_grouped_gemm_bf16(const uint16_t* A_bf16_dev, const uint16_t* W_bf16_dev, const int32_t* expert_offsets_dev,
-                           int R, int E, int N, int K, uint16_t* C_bf16_dev, void* stream);
+                           int R, int E, int N, int K, uint16_t* C_bf16_dev, void* workspace_dev, size_t workspace_bytes,
+                           void* stream);
 int w4a8_grouped_gemm_dgrad(const uint16_t* dC_bf16_dev, const uint16_t* W_bf16_dev,
                             const int32_t* expert_offsets_dev, int R, int E, int N, int K, uint16_t* dA_bf16_dev,
-                            void* stream);
+                            void* workspace_dev, size_t workspace_bytes, void* stream);
 int w4a8_grouped_gemm_wgrad(const uint16_t* dC_bf16_dev, const uint16_t* A_bf16_dev,
                             const int32_t* expert_offsets_dev, int R, int E, int N, int K, void* dW_dev, int dW_type,
-                            int accumulate, void* stream);
+                            int accumulate, void* workspace_dev, size_t workspace_bytes, void* stream);
 
 /*
  * w4a8_quantize_fp4 -- bf16 weights to the 4-bit formats of
@@ -714,6 +722,7 @@ int w4a8_quantize_gather_fp4(const uint16_t* x_bf16_dev, int T, int K, const int
  * B_fp4_dev           uint8 [E][N][K/2], b_scales_dev uint8 [E][N][K/32] E8M0.
  * expert_offsets_dev  as w4a8_grouped_gemm_bf16.
  * C_bf16_dev          out bf16 [R][N]; rows from offsets[E] on are left as they were.
+ * workspace_dev       as w4a8_grouped_gemm_bf16.
  * A scale code of 0xFF makes its row or column of the product NaN.
  * Limits: 1 <= E <= W4A8_MAX_EXPERTS, R >= 0, N % 32 == 0, 32 <= N <=
  * W4A8_MAX_N, K % 128 == 0, 128 <= K <= W4A8_MAX_K.  R == 0 does nothing.
@@ -721,7 +730,7 @@ int w4a8_quantize_gather_fp4(const uint16_t* x_bf16_dev, int T, int K, const int
  */
 int w4a8_grouped_gemm_a4(const uint8_t* A_fp4_dev, const uint8_t* a_scales_dev, const uint8_t* B_fp4_dev,
                          const uint8_t* b_scales_dev, const int32_t* expert_offsets_dev, int R, int E, int N, int K,
-                         uint16_t* C_bf16_dev, void* stream);
+                         uint16_t* C_bf16_dev, void* workspace_dev, size_t workspace_bytes, void* stream);
 
 /*
  * w4a8_clip_grads -- the norm of n tensors as one vector and their scaling by it:

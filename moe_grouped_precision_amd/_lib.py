@@ -84,9 +84,9 @@ def _declare(lib):
     lib.w4a8_rms_norm_backward_bytes.argtypes = [i32, i32]
     lib.w4a8_rms_norm_backward_bytes.restype = sz
     for f in (lib.w4a8_grouped_gemm_bf16, lib.w4a8_grouped_gemm_dgrad):
-        f.argtypes = [vp, vp, vp, i32, i32, i32, i32, vp, vp]
+        f.argtypes = [vp, vp, vp, i32, i32, i32, i32, vp, vp, sz, vp]
         f.restype = i32
-    lib.w4a8_grouped_gemm_wgrad.argtypes = [vp, vp, vp, i32, i32, i32, i32, vp, i32, i32, vp]
+    lib.w4a8_grouped_gemm_wgrad.argtypes = [vp, vp, vp, i32, i32, i32, i32, vp, i32, i32, vp, sz, vp]
     lib.w4a8_grouped_gemm_wgrad.restype = i32
     lib.w4a8_quantize_fp4.argtypes = [vp, i32, i32, i32, i32, vp, vp, vp, vp, sz, vp]
     lib.w4a8_quantize_fp4.restype = i32
@@ -96,7 +96,9 @@ def _declare(lib):
     lib.w4a8_dequantize_fp4.restype = i32
     lib.w4a8_quantize_gather_fp4.argtypes = [vp, i32, i32, vp, i32, i32, vp, vp, vp]
     lib.w4a8_quantize_gather_fp4.restype = i32
-    lib.w4a8_grouped_gemm_a4.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, vp, vp]
+    lib.w4a8_grouped_gemm_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+    lib.w4a8_grouped_gemm_workspace_bytes.restype = sz
+    lib.w4a8_grouped_gemm_a4.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, sz, vp]
     lib.w4a8_grouped_gemm_a4.restype = i32
     lib.w4a8_clip_grads.argtypes = [vp, vp, vp, vp, i32, f32, f32, vp, sz, vp, vp]
     lib.w4a8_clip_grads.restype = i32
@@ -814,6 +816,18 @@ def _product(rows: torch.Tensor, W: torch.Tensor, expert_offsets: torch.Tensor, 
     return rows.shape[0], *W.shape
 
 
+_PRODUCT_BF16, _PRODUCT_DGRAD, _PRODUCT_WGRAD, _PRODUCT_A4 = 0, 1, 2, 3
+
+
+def _product_workspace(lib, product, R, E, N, K, device):
+    """(tensor that keeps it, pointer, bytes) of a product's workspace; (None, None, 0) where it has none."""
+    need = lib.w4a8_grouped_gemm_workspace_bytes(product, R, E, N, K)
+    if not need:
+        return None, None, 0
+    work = torch.empty(need, dtype=torch.uint8, device=device)
+    return work, work.data_ptr(), need
+
+
 def grouped_gemm_bf16(A: torch.Tensor, W: torch.Tensor, expert_offsets: torch.Tensor,
                       out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """C bf16 [R, N] of the grouped product with bf16 weights: A bf16 [R, K], W
@@ -827,8 +841,9 @@ def grouped_gemm_bf16(A: torch.Tensor, W: torch.Tensor, expert_offsets: torch.Te
         out = torch.empty((R, N), dtype=_bfloat16, device=A.device)
     _bf16(out, "out", R * N)
     _here(A, W, expert_offsets, out)
+    _keep, work, work_bytes = _product_workspace(lib, _PRODUCT_BF16, R, E, N, K, A.device)
     _check("w4a8_grouped_gemm_bf16", lib.w4a8_grouped_gemm_bf16(
-        _ptr(A), _ptr(W), _ptr(expert_offsets), R, E, N, K, _ptr(out), _stream()))
+        _ptr(A), _ptr(W), _ptr(expert_offsets), R, E, N, K, _ptr(out), work, work_bytes, _stream()))
     return out
 
 
@@ -843,8 +858,9 @@ def grouped_gemm_dgrad(dC: torch.Tensor, W: torch.Tensor, expert_offsets: torch.
         out = torch.empty((R, K), dtype=_bfloat16, device=dC.device)
     _bf16(out, "out", R * K)
     _here(dC, W, expert_offsets, out)
+    _keep, work, work_bytes = _product_workspace(lib, _PRODUCT_DGRAD, R, E, N, K, dC.device)
     _check("w4a8_grouped_gemm_dgrad", lib.w4a8_grouped_gemm_dgrad(
-        _ptr(dC), _ptr(W), _ptr(expert_offsets), R, E, N, K, _ptr(out), _stream()))
+        _ptr(dC), _ptr(W), _ptr(expert_offsets), R, E, N, K, _ptr(out), work, work_bytes, _stream()))
     return out
 
 
@@ -871,9 +887,10 @@ def grouped_gemm_wgrad(dC: torch.Tensor, A: torch.Tensor, expert_offsets: torch.
     else:
         _bf16(out, "out", E * N * K)
     _here(dC, A, expert_offsets, out)
+    _keep, work, work_bytes = _product_workspace(lib, _PRODUCT_WGRAD, R, E, N, K, dC.device)
     _check("w4a8_grouped_gemm_wgrad", lib.w4a8_grouped_gemm_wgrad(
         _ptr(dC), _ptr(A), _ptr(expert_offsets), R, E, N, K, _ptr(out), 0 if out.dtype is torch.float32 else 1,
-        int(accumulate), _stream()))
+        int(accumulate), work, work_bytes, _stream()))
     return out
 
 
@@ -995,8 +1012,9 @@ def grouped_gemm_a4(A: torch.Tensor, SA: torch.Tensor, B: torch.Tensor, SB: torc
         out = torch.empty((R, N), dtype=_bfloat16, device=A.device)
     _bf16(out, "out", R * N)
     _here(A, SA, B, SB, expert_offsets, out)
+    _keep, work, work_bytes = _product_workspace(lib, _PRODUCT_A4, R, E, N, K, A.device)
     _check("w4a8_grouped_gemm_a4", lib.w4a8_grouped_gemm_a4(
-        _ptr(A), _ptr(SA), _ptr(B), _ptr(SB), _ptr(expert_offsets), R, E, N, K, _ptr(out), _stream()))
+        _ptr(A), _ptr(SA), _ptr(B), _ptr(SB), _ptr(expert_offsets), R, E, N, K, _ptr(out), work, work_bytes, _stream()))
     return out
 
 

@@ -138,7 +138,15 @@ int check_bf16_product(int R, int E, int N, int K) {
 w4a8::TileArgs bf16_product(const uint16_t* Y, const uint16_t* X, const int32_t* offsets, void* out, int E, int R,
                             int N, int K, int accumulate) {
   return {reinterpret_cast<const uint8_t*>(Y), reinterpret_cast<const uint8_t*>(X), nullptr, nullptr, offsets, out,
-          E, R, N, K, accumulate};
+          E, R, N, K, accumulate, 1, 0};
+}
+
+// A product's workspace is there whole, or not given.
+int check_workspace(int product, int R, int E, int N, int K, const void* work, size_t bytes) {
+  const size_t need = work ? w4a8::product_workspace(product, R, E, N, K) : 0;
+  if (bytes < need) return fail(W4A8_ERR_CAPACITY, "workspace of %zu bytes, %zu needed", bytes, need);
+  if (!aligned(work, 16)) return fail(W4A8_ERR_ALIGN, "the workspace needs 16-byte alignment");
+  return W4A8_OK;
 }
 
 int check_fp4(int fmt, int E, int N, int K) {
@@ -709,27 +717,37 @@ int w4a8_rms_norm_backward(const uint16_t* h_bf16_dev, const void* weight_dev, i
   return ok();
 }
 
+size_t w4a8_grouped_gemm_workspace_bytes(int product, int R, int E, int N, int K) {
+  if (product < W4A8_PRODUCT_BF16 || product > W4A8_PRODUCT_A4 || R < 1 || E < 1 || E > W4A8_MAX_EXPERTS || N < 1 ||
+      N > W4A8_MAX_N || K < 1 || K > W4A8_MAX_K)
+    return 0;
+  return w4a8::product_workspace(product, R, E, N, K);
+}
+
 int w4a8_grouped_gemm_bf16(const uint16_t* A_bf16_dev, const uint16_t* W_bf16_dev, const int32_t* expert_offsets_dev,
-                           int R, int E, int N, int K, uint16_t* C_bf16_dev, void* stream) {
+                           int R, int E, int N, int K, uint16_t* C_bf16_dev, void* workspace_dev, size_t workspace_bytes,
+                           void* stream) {
   int st = check_bf16_product(R, E, N, K);
   if (st != W4A8_OK) return st;
   if (R > 0 && (!A_bf16_dev || !W_bf16_dev || !expert_offsets_dev || !C_bf16_dev))
     return fail(W4A8_ERR_NULL, "null pointer argument");
   if (!aligned(A_bf16_dev, 2) || !aligned(W_bf16_dev, 2) || !aligned(C_bf16_dev, 2) || !aligned(expert_offsets_dev, 4))
     return fail(W4A8_ERR_ALIGN, "A, W and C need 2-byte, offsets 4-byte alignment");
+  st = check_workspace(w4a8::PRODUCT_FWD, R, E, N, K, workspace_dev, workspace_bytes);
+  if (st != W4A8_OK) return st;
   const DeviceInfo* d = nullptr;
   st = device_info(&d);
   if (st != W4A8_OK) return st;
   if (R == 0) return ok();
   hipError_t e = w4a8::launch_grouped_bf16(bf16_product(A_bf16_dev, W_bf16_dev, expert_offsets_dev, C_bf16_dev, E, R,
-                                                        N, K, 0), (hipStream_t)stream);
+                                                        N, K, 0), workspace_dev, (hipStream_t)stream);
   if (e != hipSuccess) return fail(W4A8_ERR_HIP, "grouped_gemm_bf16 launch: %s", hipGetErrorString(e));
   return ok();
 }
 
 int w4a8_grouped_gemm_dgrad(const uint16_t* dC_bf16_dev, const uint16_t* W_bf16_dev,
                             const int32_t* expert_offsets_dev, int R, int E, int N, int K, uint16_t* dA_bf16_dev,
-                            void* stream) {
+                            void* workspace_dev, size_t workspace_bytes, void* stream) {
   int st = check_bf16_product(R, E, N, K);
   if (st != W4A8_OK) return st;
   if (R > 0 && (!dC_bf16_dev || !W_bf16_dev || !expert_offsets_dev || !dA_bf16_dev))
@@ -737,19 +755,21 @@ int w4a8_grouped_gemm_dgrad(const uint16_t* dC_bf16_dev, const uint16_t* W_bf16_
   if (!aligned(dC_bf16_dev, 2) || !aligned(W_bf16_dev, 2) || !aligned(dA_bf16_dev, 2) ||
       !aligned(expert_offsets_dev, 4))
     return fail(W4A8_ERR_ALIGN, "dC, W and dA need 2-byte, offsets 4-byte alignment");
+  st = check_workspace(w4a8::PRODUCT_ROWS, R, E, N, K, workspace_dev, workspace_bytes);
+  if (st != W4A8_OK) return st;
   const DeviceInfo* d = nullptr;
   st = device_info(&d);
   if (st != W4A8_OK) return st;
   if (R == 0) return ok();
   hipError_t e = w4a8::launch_grouped_dgrad(bf16_product(dC_bf16_dev, W_bf16_dev, expert_offsets_dev, dA_bf16_dev, E,
-                                                         R, N, K, 0), (hipStream_t)stream);
+                                                         R, N, K, 0), workspace_dev, (hipStream_t)stream);
   if (e != hipSuccess) return fail(W4A8_ERR_HIP, "grouped_gemm_dgrad launch: %s", hipGetErrorString(e));
   return ok();
 }
 
 int w4a8_grouped_gemm_wgrad(const uint16_t* dC_bf16_dev, const uint16_t* A_bf16_dev,
                             const int32_t* expert_offsets_dev, int R, int E, int N, int K, void* dW_dev, int dW_type,
-                            int accumulate, void* stream) {
+                            int accumulate, void* workspace_dev, size_t workspace_bytes, void* stream) {
   int st = check_bf16_product(R, E, N, K);
   if (st != W4A8_OK) return st;
   if (dW_type != W4A8_TYPE_F32 && dW_type != W4A8_TYPE_BF16)
@@ -759,12 +779,14 @@ int w4a8_grouped_gemm_wgrad(const uint16_t* dC_bf16_dev, const uint16_t* A_bf16_
   if (!aligned(dC_bf16_dev, 2) || !aligned(A_bf16_dev, 2) || !aligned(dW_dev, dW_type == W4A8_TYPE_F32 ? 4 : 2) ||
       !aligned(expert_offsets_dev, 4))
     return fail(W4A8_ERR_ALIGN, "dC and A need 2-byte, dW its type's, offsets 4-byte alignment");
+  st = check_workspace(w4a8::PRODUCT_WEIGHTS, R, E, N, K, workspace_dev, workspace_bytes);
+  if (st != W4A8_OK) return st;
   const DeviceInfo* d = nullptr;
   st = device_info(&d);
   if (st != W4A8_OK) return st;
   hipError_t e = w4a8::launch_grouped_wgrad(bf16_product(dC_bf16_dev, A_bf16_dev, expert_offsets_dev, dW_dev, E, R, N,
                                                          K, accumulate != 0),
-                                            dW_type == W4A8_TYPE_F32, (hipStream_t)stream);
+                                            dW_type == W4A8_TYPE_F32, workspace_dev, (hipStream_t)stream);
   if (e != hipSuccess) return fail(W4A8_ERR_HIP, "grouped_gemm_wgrad launch: %s", hipGetErrorString(e));
   return ok();
 }
@@ -840,7 +862,7 @@ int w4a8_quantize_gather_fp4(const uint16_t* x_bf16_dev, int T, int K, const int
 
 int w4a8_grouped_gemm_a4(const uint8_t* A_fp4_dev, const uint8_t* a_scales_dev, const uint8_t* B_fp4_dev,
                          const uint8_t* b_scales_dev, const int32_t* expert_offsets_dev, int R, int E, int N, int K,
-                         uint16_t* C_bf16_dev, void* stream) {
+                         uint16_t* C_bf16_dev, void* workspace_dev, size_t workspace_bytes, void* stream) {
   int st = check_gemm_shape(E, N, K);
   if (st != W4A8_OK) return st;
   if (R < 0) return fail(W4A8_ERR_SHAPE, "R=%d", R);
@@ -849,13 +871,15 @@ int w4a8_grouped_gemm_a4(const uint8_t* A_fp4_dev, const uint8_t* a_scales_dev, 
   if (!aligned(A_fp4_dev, 16) || !aligned(B_fp4_dev, 16) || !aligned(C_bf16_dev, 16) || !aligned(a_scales_dev, 4) ||
       !aligned(b_scales_dev, 4) || !aligned(expert_offsets_dev, 4))
     return fail(W4A8_ERR_ALIGN, "A, B, C need 16-byte and scales/offsets 4-byte alignment");
+  st = check_workspace(w4a8::PRODUCT_FOUR, R, E, N, K, workspace_dev, workspace_bytes);
+  if (st != W4A8_OK) return st;
   const DeviceInfo* d = nullptr;
   st = device_info(&d);
   if (st != W4A8_OK) return st;
   if (R == 0) return ok();
   const w4a8::TileArgs args{A_fp4_dev, B_fp4_dev, a_scales_dev, b_scales_dev, expert_offsets_dev, C_bf16_dev,
-                            E, R, N, K, 0};
-  hipError_t e = w4a8::launch_grouped_a4(args, (hipStream_t)stream);
+                            E, R, N, K, 0, 1, 0};
+  hipError_t e = w4a8::launch_grouped_a4(args, workspace_dev, (hipStream_t)stream);
   if (e != hipSuccess) return fail(W4A8_ERR_HIP, "grouped_gemm_a4 launch: %s", hipGetErrorString(e));
   return ok();
 }

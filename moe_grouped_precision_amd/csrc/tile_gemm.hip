@@ -34,7 +34,8 @@ typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 
-enum { FWD = 0, ROWS = 1, WEIGHTS = 2, FOUR = 3 };
+enum { FWD = PRODUCT_FWD, ROWS = PRODUCT_ROWS, WEIGHTS = PRODUCT_WEIGHTS, FOUR = PRODUCT_FOUR };
+constexpr int FEW_ROWS = 48, MANY_ROWS = 768;   // of an expert in the mean: see launch_bf16
 
 // What a chunk past the end of z is read from: zeros, so that whatever the
 // buffer holds there (another expert's rows, infinities) stays out of the sums.
@@ -124,16 +125,17 @@ __device__ __forceinline__ bool find_tile(const TileArgs& a, int64_t b, Place& p
   int64_t t;
   int m = 0, e = 0, mine = fixed;
   if (MODE == WEIGHTS) {
-    // a tile costs what its expert has rows: every XCD gets an eighth of each expert
+    // a tile costs what its expert has rows: every XCD gets an eighth of each
+    // expert, the first one another XCD each time (it may be all there is)
     const int all = fixed * nt, per = (all + 7) >> 3;
     const int64_t j = b >> 3;
     e = (int)(j / per);
-    t = (b & 7) * per + (j - (int64_t)e * per);
+    t = ((b + e + blockIdx.y) & 7) * per + (j - (int64_t)e * per);
     if (e >= a.E || t >= all) return false;
   } else {
     const int64_t total = (int64_t)__builtin_amdgcn_readlane(wave_inclusive_sum(sum), 63) * nt;
     const int64_t per = (total + 7) >> 3;
-    t = (b & 7) * per + (b >> 3);
+    t = ((b + blockIdx.y) & 7) * per + (b >> 3);
     if ((b >> 3) >= per || t >= total) return false;
     m = (int)(t / nt);   // row tiles before the expert's are whole rows of nt tiles
     int before = 0;
@@ -174,18 +176,31 @@ __device__ __forceinline__ bool find_tile(const TileArgs& a, int64_t b, Place& p
   return true;
 }
 
-// 16 bytes of a row at any 2-byte alignment; n < 8 values from its end one by
-// one, none past it.
+// 16 bytes of a row at any 2-byte alignment, n of its 8 values.  The last ones of
+// a row are the row's last 16 bytes, moved down by `only` when they are used: a
+// load under a condition has to be waited for where the condition ends.
 __device__ __forceinline__ v4i load_any(const uint8_t* p, int n) {
+  v4i v;
+  const uint8_t* q = n <= 0 ? reinterpret_cast<const uint8_t*>(&zero_chunk) : p - 2 * (8 - min(n, 8));
+  __builtin_memcpy(&v, q, 16);
+  return v;
+}
+__device__ __forceinline__ v4i only(v4i v, int n) {
+  const int by = n <= 0 || n >= 8 ? 0 : 8 - n;
+  if (by & 4) v = (v4i){v[2], v[3], 0, 0};
+  if (by & 2) v = (v4i){v[1], v[2], v[3], 0};
+  if (by & 1)
+    v = (v4i){(int)__builtin_amdgcn_alignbit(v[1], v[0], 16), (int)__builtin_amdgcn_alignbit(v[2], v[1], 16),
+              (int)__builtin_amdgcn_alignbit(v[3], v[2], 16), (int)((uint32_t)v[3] >> 16)};
+  return v;
+}
+// Rows of fewer than 8 values, one by one.
+__device__ __forceinline__ v4i load_few(const uint8_t* p, int n) {
   v4i v = {0, 0, 0, 0};
-  if (n >= 8) {
-    __builtin_memcpy(&v, p, 16);
-  } else {
-    const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
+  const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
 #pragma unroll
-    for (int i = 0; i < 7; ++i)
-      if (i < n) v[i >> 1] |= (int)((uint32_t)q[i] << (16 * (i & 1)));
-  }
+  for (int i = 0; i < 7; ++i)
+    if (i < n) v[i >> 1] |= (int)((uint32_t)q[i] << (16 * (i & 1)));
   return v;
 }
 
@@ -198,46 +213,64 @@ __device__ __forceinline__ void chunk_of(int j, int lane, int& row, int& chunk) 
   chunk = (lane % CPR) ^ (TR ? swz<T>(row) : key<KS>(row & 15));
 }
 
-// What the kernels of one product have in common.
+// What the kernels of one product have in common.  With a.slices > 1 a workgroup
+// takes one slice of z (blockIdx.y, whole steps), into an array of its own.
 template <int MODE>
 struct Operands {
   static constexpr bool YT = MODE == WEIGHTS, XT = MODE == WEIGHTS || MODE == ROWS;   // transposed operands
-  const uint8_t *Y, *X;   // of the tile, at z = 0
+  const uint8_t *Y, *X;   // of the tile, at the first z
   int ybytes, xbytes;     // from row to row
   int zn;                 // extent of z
   int width;              // of the output
+  size_t out0;            // the slice's array
   __device__ __forceinline__ Operands(const TileArgs& a, const Place& p) {
     zn = MODE == WEIGHTS ? p.rows : MODE == ROWS ? a.N : a.K;
     ybytes = MODE == FOUR ? a.K / 2 : MODE == FWD ? a.K * 2 : a.N * 2;
     xbytes = MODE == FOUR ? a.K / 2 : a.K * 2;
+    width = MODE == ROWS || MODE == WEIGHTS ? a.K : a.N;
     Y = a.Y + (size_t)(p.r0 + (MODE == WEIGHTS ? 0 : p.y0)) * ybytes + (MODE == WEIGHTS ? p.y0 * 2 : 0);
     X = MODE == WEIGHTS ? a.X + (size_t)p.r0 * xbytes + p.x0 * 2
         : MODE == ROWS  ? a.X + (size_t)p.e * a.N * xbytes + p.x0 * 2
                         : a.X + ((size_t)p.e * a.N + p.x0) * xbytes;
-    width = MODE == ROWS || MODE == WEIGHTS ? a.K : a.N;
+    out0 = 0;
+    if (a.slices > 1) {
+      const int z0 = min(zn, (int)blockIdx.y * slice_of(zn, a.slices));
+      zn = min(zn - z0, slice_of(zn, a.slices));
+      Y += YT ? (size_t)z0 * ybytes : MODE == FOUR ? z0 / 2 : z0 * 2;
+      X += XT ? (size_t)z0 * xbytes : MODE == FOUR ? z0 / 2 : z0 * 2;
+      out0 = (size_t)blockIdx.y * (MODE == WEIGHTS ? (size_t)a.E * a.N : (size_t)a.R) * width;
+    }
+  }
+  static __device__ __forceinline__ int slice_of(int z, int slices) {
+    constexpr int STEP = MODE == FOUR ? 512 : 64;
+    return (z / slices + STEP) / STEP * STEP;   // slices * this > z
   }
 };
 
-// The lane's results of one 16 x 16 block to out[y][x .. x+3].
-template <int MODE, bool WHOLE, typename OUT>
-__device__ __forceinline__ void put(const TileArgs& a, const Place& p, int width, int y, int x, v4f v) {
+// Four of the lane's results to out[y][x .. x+3].
+template <int MODE, typename OUT>
+__device__ __forceinline__ void put(const TileArgs& a, const Place& p, const Operands<MODE>& op, int y, int x, v4f v) {
   if (y >= p.ny || x >= p.nx) return;
-  OUT* o = static_cast<OUT*>(a.out) +
-           (MODE == WEIGHTS ? (size_t)p.e * a.N + p.y0 + y : (size_t)(p.r0 + p.y0 + y)) * width + p.x0 + x;
-  const int n = WHOLE ? 4 : min(4, p.nx - x);
+  OUT* o = static_cast<OUT*>(a.out) + op.out0 +
+           (MODE == WEIGHTS ? (size_t)p.e * a.N + p.y0 + y : (size_t)(p.r0 + p.y0 + y)) * op.width + p.x0 + x;
+  const int n = a.wide ? 4 : min(4, p.nx - x);
   if (MODE == WEIGHTS && a.accumulate) {
 #pragma unroll
     for (int c = 0; c < 4; ++c)
       if (c < n) v[c] += sizeof(OUT) == 4 ? (float)o[c] : __uint_as_float((uint32_t)(uint16_t)o[c] << 16);
   }
   if constexpr (sizeof(OUT) == 4) {
-    if (WHOLE) *reinterpret_cast<v4f*>(o) = v;
+    if (a.wide) *reinterpret_cast<v4f*>(o) = v;
     else
-      for (int c = 0; c < n; ++c) o[c] = v[c];
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (c < n) o[c] = v[c];
   } else {
-    if (WHOLE) store_bf16x4(o, v);
+    if (a.wide) store_bf16x4(o, v);
     else
-      for (int c = 0; c < n; ++c) o[c] = __builtin_bit_cast(uint16_t, (__bf16)v[c]);
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (c < n) o[c] = __builtin_bit_cast(uint16_t, (__bf16)v[c]);
   }
 }
 
@@ -247,7 +280,9 @@ __device__ __forceinline__ v4f mfma_bf16(v4i x, v4i y, v4f acc) {
 
 // ---------------------------------------------------------------------------
 // Rows that are no whole 16-byte chunks at 16-byte addresses: through registers,
-// 128 x 128 tiles, steps of 32 z, two of them in LDS.
+// 128 x 128 tiles, steps of 32 z, two of them in LDS and two on their way.  Bound
+// by the loads at 2-byte addresses and the writes to LDS: 200 to 250 TFLOP/s
+// (weights' gradient of 11365 rows, 45 experts, 4440 x 2165: 980 us).
 // ---------------------------------------------------------------------------
 template <int MODE, typename OUT>
 struct General {
@@ -291,29 +326,39 @@ struct General {
       }
     }
     const size_t ystep = YT ? (size_t)32 * op.ybytes : 64, xstep = XT ? (size_t)32 * op.xbytes : 64;
-    v4i reg[2 * NI];
-    auto fetch = [&](int s) {
+    // two steps ahead in registers, one in LDS: a step takes as long as the way to
+    // memory where there are few tiles
+    v4i reg[2][2 * NI];
+    const bool few_y = op.ybytes < 16, few_x = op.xbytes < 16;
+    // values of chunk i in step s
+    auto values = [&](int i, int s) {
+      const int z = left[i] - 32 * s;
+      return (i < NI ? YT : XT) ? (z > 0 ? wide[i] : 0) : z;
+    };
+    auto fetch = [&](int s, int to) {
 #pragma unroll
       for (int i = 0; i < 2 * NI; ++i) {
-        const int z = left[i] - 32 * s;
-        reg[i] = load_any(src[i], z <= 0 ? 0 : (i < NI ? YT : XT) ? wide[i] : z);
+        const int n = values(i, s);
+        if (i < NI ? few_y : few_x) reg[to][i] = load_few(src[i], n);
+        else reg[to][i] = load_any(src[i], n);
         src[i] += i < NI ? ystep : xstep;
       }
     };
-    auto fill = [&](uint32_t stage) {
+    // which operands have such ends, in any step or in the last
+    const bool end_y = !few_y && (YT ? (p.ny & 7) != 0 : (op.zn & 7) != 0);
+    const bool end_x = !few_x && (XT ? (p.nx & 7) != 0 : (op.zn & 7) != 0);
+    auto fill = [&](int s, int from) {
 #pragma unroll
-      for (int i = 0; i < 2 * NI; ++i)
-        *(lds_v4i*)(uintptr_t)(stage + (i / NI) * TY * 64 + (wave + NW * (i % NI)) * 1024 + lane * 16) = reg[i];
+      for (int i = 0; i < 2 * NI; ++i) {
+        if ((i < NI ? end_y : end_x) && ((i < NI ? YT : XT) || s == steps - 1)) reg[from][i] = only(reg[from][i], values(i, s));
+        *(lds_v4i*)(uintptr_t)(lds + from * STAGE + (i / NI) * TY * 64 + (wave + NW * (i % NI)) * 1024 + lane * 16) =
+            reg[from][i];
+      }
     };
     const int wy = wave >> 1, wx = wave & 1;
-    if (steps > 0) {
-      fetch(0);
-      fill(lds);
-      __syncthreads();
-    }
-    for (int s = 0; s < steps; ++s) {
-      if (s + 1 < steps) fetch(s + 1);
-      const uint32_t stage = lds + (s & 1) * STAGE;
+    auto step = [&](int s, int at) {   // at = s & 1
+      if (s + 2 < steps) fetch(s + 2, at);
+      const uint32_t stage = lds + at * STAGE;
       v4i fy[M], fx[M];
 #pragma unroll
       for (int i = 0; i < M; ++i) {
@@ -326,16 +371,25 @@ struct General {
       for (int i = 0; i < M; ++i)
 #pragma unroll
         for (int j = 0; j < M; ++j) acc[i][j] = mfma_bf16(fx[j], fy[i], acc[i][j]);
-      if (s + 1 < steps) fill(lds + ((s + 1) & 1) * STAGE);
+      if (s + 1 < steps) fill(s + 1, at ^ 1);
       __syncthreads();
+    };
+    if (steps > 0) {
+      fetch(0, 0);
+      if (steps > 1) fetch(1, 1);
+      fill(0, 0);
+      __syncthreads();
+    }
+    for (int s = 0; s < steps; s += 2) {
+      step(s, 0);
+      if (s + 1 < steps) step(s + 1, 1);
     }
     if (MODE == WEIGHTS && a.accumulate && steps == 0) return;
 #pragma unroll
     for (int i = 0; i < M; ++i)
 #pragma unroll
       for (int j = 0; j < M; ++j)
-        put<MODE, false, OUT>(a, p, op.width, (wy * M + i) * 16 + (lane & 15), (wx * M + j) * 16 + 4 * (lane >> 4),
-                              acc[i][j]);
+        put<MODE, OUT>(a, p, op, (wy * M + i) * 16 + (lane & 15), (wx * M + j) * 16 + 4 * (lane >> 4), acc[i][j]);
   }
 };
 
@@ -422,15 +476,17 @@ struct Direct {
     };
     advance(0);
     // FP4: the codes of steps s and s + 1, 4 lanes per row
+    const uint8_t* xrow = a.X + ((size_t)p.e * a.N + p.x0) * op.xbytes;
     auto load_scales = [&](int s) {
-      const int g = a.K / 32, word = 2 * s + (lane & 3);   // of 128 z
+      // of 128 z, from the slice's first on
+      const int g = a.K / 32, word = 2 * s + (lane & 3), word0 = (int)(op.X - xrow) / 64;
 #pragma unroll
       for (int i = 0; i < IS; ++i) {
         const int j = wave * IS + i, row = j * 16 + (lane >> 2);   // TY % 16 == 0: a load is of one operand
         const bool isy = j * 16 < TY;
         const uint8_t* q = isy ? a.SY + (size_t)(p.r0 + p.y0 + min(row, p.ny - 1)) * g
                                : a.SX + ((size_t)p.e * a.N + p.x0 + min(row - TY, p.nx - 1)) * g;
-        vm_dma4(word * 128 < op.zn ? q + word * 4 : reinterpret_cast<const uint8_t*>(&zero_chunk),
+        vm_dma4(word * 128 < op.zn ? q + (word0 + word) * 4 : reinterpret_cast<const uint8_t*>(&zero_chunk),
                 lds + STAGE * NS + ((s >> 1) & 1) * SCALES + j * 256);
       }
     };
@@ -565,8 +621,7 @@ struct Direct {
     for (int i = 0; i < MY; ++i)
 #pragma unroll
       for (int j = 0; j < MX; ++j)
-        put<MODE, true, OUT>(a, p, op.width, (i * WY + wy) * 16 + (lane & 15), (wx * MX + j) * 16 + 4 * (lane >> 4),
-                             acc[i][j]);
+        put<MODE, OUT>(a, p, op, (i * WY + wy) * 16 + (lane & 15), (wx * MX + j) * 16 + 4 * (lane >> 4), acc[i][j]);
   }
 };
 
@@ -575,6 +630,16 @@ __global__ void __launch_bounds__(T::THREADS, T::PER_SIMD)
 tile_kernel(TileArgs a, int64_t b0) {
   extern __shared__ __align__(1024) uint8_t smem[];
   T::run(a, b0 + blockIdx.x, lds_u32(smem));
+}
+
+// Workgroups of a product: tiles are known for the weights, otherwise at most
+// (each expert's last may be part of one); they come in eights, one per XCD.
+template <int MODE>
+int64_t workgroups(const TileArgs& a, int TY, int TX) {
+  const int64_t width = MODE == ROWS || MODE == WEIGHTS ? a.K : a.N, nt = (width + TX - 1) / TX;
+  const int64_t eights = MODE == WEIGHTS ? a.E * (((a.N + TY - 1) / TY * nt + 7) / 8)
+                                         : ((a.R + (int64_t)std::min(a.E, a.R) * (TY - 1)) / TY * nt + 7) / 8;
+  return eights * 8;
 }
 
 template <int MODE, typename T>
@@ -593,17 +658,73 @@ hipError_t launch(const TileArgs& a, hipStream_t stream) {
       allowed.fetch_or(bit, std::memory_order_release);
     }
   }
-  // tiles: known for the weights, otherwise at most (each expert's last may be
-  // part of one); workgroups come in eights, one per XCD
-  const int64_t width = MODE == ROWS || MODE == WEIGHTS ? a.K : a.N, nt = (width + T::TX - 1) / T::TX;
-  const int64_t eights = MODE == WEIGHTS ? a.E * (((a.N + T::TY - 1) / T::TY * nt + 7) / 8)
-                                         : ((a.R + (int64_t)std::min(a.E, a.R) * (T::TY - 1)) / T::TY * nt + 7) / 8;
-  return in_launches(eights * 8, T::THREADS, [&](int64_t b, int64_t n) {
-    hipLaunchKernelGGL(tile_kernel<T>, dim3((unsigned)n), dim3(T::THREADS), T::LDS, stream, a, b);
+  return in_launches(workgroups<MODE>(a, T::TY, T::TX), T::THREADS, [&](int64_t b, int64_t n) {
+    hipLaunchKernelGGL(tile_kernel<T>, dim3((unsigned)n, a.slices), dim3(T::THREADS), T::LDS, stream, a, b);
   });
 }
 
-bool chunks16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+// The slices' sums to the output, in the slices' order: flat, from the first row
+// on to the last that the offsets give.
+template <int MODE, typename OUT>
+__global__ void __launch_bounds__(256)
+join_kernel(TileArgs a, const float* __restrict__ parts) {
+  __shared__ int bad;
+  if (threadIdx.x == 0) bad = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < a.E; i += blockDim.x) {
+    const int o0 = a.offsets[i], o1 = a.offsets[i + 1];
+    if (o1 < o0 || (i == 0 && o0 != 0) || (i == a.E - 1 && o1 > a.R)) bad = 1;
+  }
+  __syncthreads();
+  if (bad) return;
+  const size_t width = MODE == ROWS || MODE == WEIGHTS ? a.K : a.N;
+  const size_t all = (MODE == WEIGHTS ? (size_t)a.E * a.N : (size_t)a.R) * width;
+  const size_t n = MODE == WEIGHTS ? all : (size_t)a.offsets[a.E] * width;
+  OUT* out = static_cast<OUT*>(a.out);
+  for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (size_t)gridDim.x * blockDim.x) {
+    float v = 0.f;
+    for (int s0 = 0; s0 < a.slices; s0 += 16) {   // 16 loads on their way
+      float part[16];
+#pragma unroll
+      for (int s = 0; s < 16; ++s) part[s] = s0 + s < a.slices ? parts[(s0 + s) * all + i] : 0.f;
+#pragma unroll
+      for (int s = 0; s < 16; ++s) v += part[s];
+    }
+    if (MODE == WEIGHTS && a.accumulate)
+      v += sizeof(OUT) == 4 ? (float)out[i] : __uint_as_float((uint32_t)(uint16_t)out[i] << 16);
+    if constexpr (sizeof(OUT) == 4) out[i] = v;
+    else out[i] = __builtin_bit_cast(uint16_t, (__bf16)v);
+  }
+}
+
+bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+template <typename OUT>
+bool wide_out(const TileArgs& a, int width) { return width % 4 == 0 && aligned_to(a.out, 4 * sizeof(OUT)); }
+
+// Where a product has fewer tiles than the chip has CUs and a long sum, the sum is
+// cut into slices (parts of fp32 in the workspace, added in order): 3 rows, 128 x
+// 5969, 112 us in one piece and 18 in 23; the row gradient of 36 rows, 4848 x 102,
+// 246 and 19.
+template <int MODE, typename OUT, typename F>
+hipError_t launch_sliced(TileArgs a, void* work, hipStream_t stream, F launch_tiles) {
+  const int width = MODE == ROWS || MODE == WEIGHTS ? a.K : a.N;
+  a.slices = work ? product_slices(MODE, a.R, a.E, a.N, a.K) : 1;
+  if (a.slices == 1) {
+    a.wide = wide_out<OUT>(a, width);
+    return launch_tiles(a, OUT());
+  }
+  TileArgs part = a;
+  part.out = work;
+  part.accumulate = 0;
+  part.wide = wide_out<float>(part, width);
+  const hipError_t e = launch_tiles(part, float());
+  if (e != hipSuccess) return e;
+  const int64_t n = (MODE == WEIGHTS ? (int64_t)a.E * a.N : (int64_t)a.R) * width;
+  const unsigned grid = (unsigned)std::min<int64_t>((n + 255) / 256, 2048);
+  hipLaunchKernelGGL((join_kernel<MODE, OUT>), dim3(grid), dim3(256), 0, stream, a, static_cast<const float*>(work));
+  return hipGetLastError();
+}
 
 // Tiles by the mean number of rows of an expert (all that the host knows).
 // 4096 x 6144, 32 experts, unevenly filled, us a call, forward | row gradient:
@@ -618,32 +739,92 @@ bool chunks16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0
 // 288: 1133 / 1253, 1024: 2070 / 2282).
 template <int MODE, typename OUT>
 hipError_t launch_bf16(const TileArgs& a, hipStream_t stream) {
+  // Whole chunks: along K of the forward product's rows, along both of the others.
   // A tile's offsets within an operand are 32 bits: 256 rows, or 64 of z, of 8 MB
   // at most.
-  if (a.N % 8 || a.K % 8 || !chunks16(a.Y) || !chunks16(a.X) || !chunks16(a.out) || a.N > (1 << 22))
+  if (a.K % 8 || (MODE != FWD && a.N % 8) || !aligned_to(a.Y, 16) || !aligned_to(a.X, 16) || a.N > (1 << 22))
     return launch<MODE, General<MODE, OUT>>(a, stream);
   const int rows = a.R / a.E;
   if constexpr (MODE == FWD)
-    if (rows <= 48) return launch<MODE, Direct<MODE, 64, 128, 1, 4, 3, OUT>>(a, stream);
+    if (rows <= FEW_ROWS) return launch<MODE, Direct<MODE, 64, 128, 1, 4, 3, OUT>>(a, stream);
   if constexpr (MODE != WEIGHTS)
-    if (rows <= 768) return launch<MODE, Direct<MODE, 128, 256, 2, 4, 3, OUT>>(a, stream);
+    if (rows <= MANY_ROWS) return launch<MODE, Direct<MODE, 128, 256, 2, 4, 3, OUT>>(a, stream);
   return launch<MODE, Direct<MODE, 256, 256, 2, 4, 2, OUT>>(a, stream);
+}
+
+template <typename OUT>
+hipError_t launch_four(const TileArgs& a, hipStream_t stream) {
+  // as above; 16 rows: 84, 88 and 108 us with these three, 64: 134, 125 and 125,
+  // 128: 186, 159 and 170, 288: 311, 243 and 239, 1024: 882, 671 and 576
+  const int rows = a.R / a.E;
+  if (rows <= 32) return launch<FOUR, Direct<FOUR, 64, 128, 1, 4, 2, OUT>>(a, stream);
+  if (rows <= 200) return launch<FOUR, Direct<FOUR, 128, 128, 2, 2, 2, OUT>>(a, stream);
+  return launch<FOUR, Direct<FOUR, 256, 256, 2, 4, 2, OUT>>(a, stream);
 }
 
 }  // namespace
 
-hipError_t launch_grouped_bf16(const TileArgs& a, hipStream_t stream) { return launch_bf16<FWD, uint16_t>(a, stream); }
-hipError_t launch_grouped_dgrad(const TileArgs& a, hipStream_t stream) { return launch_bf16<ROWS, uint16_t>(a, stream); }
-hipError_t launch_grouped_wgrad(const TileArgs& a, bool f32, hipStream_t stream) {
-  return f32 ? launch_bf16<WEIGHTS, float>(a, stream) : launch_bf16<WEIGHTS, uint16_t>(a, stream);
+int product_slices(int mode, int R, int E, int N, int K) {
+  if (R < 1) return 1;
+  TileArgs a{};
+  a.R = R;
+  a.E = E;
+  a.N = N;
+  a.K = K;
+  const int rows = R / E;
+  int64_t tiles, z, out, most = 1 << 22;   // values of all parts: 16 MB take no longer than a launch
+  int least = 256;                         // z of a slice
+  if (mode == FWD) {
+    tiles = rows <= FEW_ROWS ? workgroups<FWD>(a, 64, 128) : workgroups<FWD>(a, 128, 256);
+    z = K;
+    out = (int64_t)R * N;
+  } else if (mode == ROWS) {
+    tiles = workgroups<ROWS>(a, 128, 256);
+    z = N;
+    out = (int64_t)R * K;
+  } else if (mode == WEIGHTS) {
+    // one expert may have most of the rows: slices as if it were four times the
+    // mean, up to four times the CUs, and parts of up to 1 KB for each row (46000
+    // rows unevenly to 26 experts, 1446 x 62: 1465 us in one piece, 133 in 4)
+    tiles = ((int64_t)E * ((N + 255) / 256) * ((K + 255) / 256) + 3) / 4;
+    z = std::min<int64_t>(R, (int64_t)rows * 4);
+    most = std::max<int64_t>(most, (int64_t)R << 8);
+    out = (int64_t)E * N * K;
+  } else {
+    tiles = rows <= 32 ? workgroups<FOUR>(a, 64, 128) : workgroups<FOUR>(a, 128, 128);
+    z = K;
+    out = (int64_t)R * N;
+    least = 1024;
+  }
+  const int64_t s = std::min({(int64_t)64, z / least, 256 / tiles, most / std::max<int64_t>(1, out)});   // 256 CUs
+  return (int)std::max<int64_t>(1, s);
 }
-hipError_t launch_grouped_a4(const TileArgs& a, hipStream_t stream) {
-  // as above; 16 rows: 84, 88 and 108 us with these three, 64: 134, 125 and 125,
-  // 128: 186, 159 and 170, 288: 311, 243 and 239, 1024: 882, 671 and 576
-  const int rows = a.R / a.E;
-  if (rows <= 32) return launch<FOUR, Direct<FOUR, 64, 128, 1, 4, 2, uint16_t>>(a, stream);
-  if (rows <= 200) return launch<FOUR, Direct<FOUR, 128, 128, 2, 2, 2, uint16_t>>(a, stream);
-  return launch<FOUR, Direct<FOUR, 256, 256, 2, 4, 2, uint16_t>>(a, stream);
+
+size_t product_workspace(int mode, int R, int E, int N, int K) {
+  const int s = product_slices(mode, R, E, N, K);
+  const size_t out = mode == FWD || mode == FOUR ? (size_t)R * N : mode == ROWS ? (size_t)R * K : (size_t)E * N * K;
+  return s == 1 ? 0 : s * out * sizeof(float);
+}
+
+hipError_t launch_grouped_bf16(const TileArgs& a, void* work, hipStream_t stream) {
+  return launch_sliced<FWD, uint16_t>(a, work, stream, [&](const TileArgs& t, auto out) {
+    return launch_bf16<FWD, decltype(out)>(t, stream);
+  });
+}
+hipError_t launch_grouped_dgrad(const TileArgs& a, void* work, hipStream_t stream) {
+  return launch_sliced<ROWS, uint16_t>(a, work, stream, [&](const TileArgs& t, auto out) {
+    return launch_bf16<ROWS, decltype(out)>(t, stream);
+  });
+}
+hipError_t launch_grouped_wgrad(const TileArgs& a, bool f32, void* work, hipStream_t stream) {
+  const auto tiles = [&](const TileArgs& t, auto out) { return launch_bf16<WEIGHTS, decltype(out)>(t, stream); };
+  return f32 ? launch_sliced<WEIGHTS, float>(a, work, stream, tiles)
+             : launch_sliced<WEIGHTS, uint16_t>(a, work, stream, tiles);
+}
+hipError_t launch_grouped_a4(const TileArgs& a, void* work, hipStream_t stream) {
+  return launch_sliced<FOUR, uint16_t>(a, work, stream, [&](const TileArgs& t, auto out) {
+    return launch_four<decltype(out)>(t, stream);
+  });
 }
 
 }  // namespace w4a8

@@ -150,10 +150,16 @@ struct TileArgs {
   const int32_t* offsets;  // [E+1]
   void* out;
   int E, R, N, K, accumulate;
+  int slices, wide;        // of z; outputs in whole 4s (both set at the launch)
 };
-hipError_t launch_grouped_bf16(const TileArgs& args, hipStream_t stream);
-hipError_t launch_grouped_dgrad(const TileArgs& args, hipStream_t stream);
-hipError_t launch_grouped_wgrad(const TileArgs& args, bool f32, hipStream_t stream);
-hipError_t launch_grouped_a4(const TileArgs& args, hipStream_t stream);
+enum { PRODUCT_FWD = 0, PRODUCT_ROWS = 1, PRODUCT_WEIGHTS = 2, PRODUCT_FOUR = 3 };
+// Slices of a product's sum, and the bytes of their parts (0 for one slice).
+int product_slices(int product, int R, int E, int N, int K);
+size_t product_workspace(int product, int R, int E, int N, int K);
+// work: product_workspace() bytes, or null for one slice in any case
+hipError_t launch_grouped_bf16(const TileArgs& args, void* work, hipStream_t stream);
+hipError_t launch_grouped_dgrad(const TileArgs& args, void* work, hipStream_t stream);
+hipError_t launch_grouped_wgrad(const TileArgs& args, bool f32, void* work, hipStream_t stream);
+hipError_t launch_grouped_a4(const TileArgs& args, void* work, hipStream_t stream);
 
 }  // namespace w4a8

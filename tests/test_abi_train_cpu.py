@@ -63,7 +63,7 @@ def test_rms_norm_backward(lib):
 
 @pytest.mark.parametrize("name", ["w4a8_grouped_gemm_bf16", "w4a8_grouped_gemm_dgrad"])
 def test_grouped_bf16(lib, name):
-    c = _caller(getattr(lib, name), (P, P, P, 16, 4, 64, 32, P, NUL))
+    c = _caller(getattr(lib, name), (P, P, P, 16, 4, 64, 32, P, NUL, 0, NUL))
     assert c(a3=-1) == SHAPE and c(a4=0) == SHAPE and c(a4=2049) == SHAPE
     assert c(a5=0) == SHAPE and c(a5=(1 << 24) + 1) == SHAPE and c(a6=0) == SHAPE and c(a6=(1 << 20) + 1) == SHAPE
     assert all(c(**{f"a{i}": NUL}) == NULL for i in (0, 1, 2, 7))
@@ -71,12 +71,26 @@ def test_grouped_bf16(lib, name):
 
 
 def test_grouped_wgrad(lib):
-    c = _caller(lib.w4a8_grouped_gemm_wgrad, (P, P, P, 16, 4, 64, 32, P, 0, 0, NUL))
+    c = _caller(lib.w4a8_grouped_gemm_wgrad, (P, P, P, 16, 4, 64, 32, P, 0, 0, NUL, 0, NUL))
     assert c(a3=-1) == SHAPE and c(a4=0) == SHAPE and c(a4=2049) == SHAPE and c(a5=0) == SHAPE and c(a6=0) == SHAPE
     assert c(a8=2) == LAYOUT and c(a8=-1) == LAYOUT
     assert all(c(**{f"a{i}": NUL}) == NULL for i in (0, 1, 2, 7)) and c(a3=0, a7=NUL) == NULL
     assert c(a0=P1) == ALIGN and c(a1=P1) == ALIGN and c(a2=P2) == ALIGN and c(a7=P2) == ALIGN
     assert c(a7=P1, a8=1) == ALIGN
+
+
+def test_product_workspaces(lib):
+    need = lib.w4a8_grouped_gemm_workspace_bytes
+    assert need(0, 16, 4, 64, 32) == 0 and need(0, 3, 2, 128, 6000) == 23 * 3 * 128 * 4
+    assert need(1, 3, 2, 6000, 128) == 23 * 3 * 128 * 4 and need(2, 8192, 1, 64, 64) == 32 * 64 * 64 * 4
+    assert need(3, 3, 2, 128, 8192) == 8 * 3 * 128 * 4
+    assert need(4, 3, 2, 128, 6000) == 0 and need(-1, 3, 2, 128, 6000) == 0 and need(0, 0, 2, 128, 6000) == 0
+    for f, a in ((lib.w4a8_grouped_gemm_bf16, (P, P, P, 3, 2, 128, 6000, P)),
+                 (lib.w4a8_grouped_gemm_dgrad, (P, P, P, 3, 2, 6000, 128, P)),
+                 (lib.w4a8_grouped_gemm_wgrad, (P, P, P, 8192, 1, 64, 64, P, 0, 0)),
+                 (lib.w4a8_grouped_gemm_a4, (P, P, P, P, P, 3, 2, 128, 8192, P))):
+        assert f(*a, Q, 64, NUL) == CAPACITY
+        assert f(*a, P8, 1 << 30, NUL) == ALIGN
 
 
 def test_quantize_fp4(lib):
@@ -107,7 +121,7 @@ def test_quantize_gather_fp4(lib):
 
 
 def test_grouped_a4(lib):
-    c = _caller(lib.w4a8_grouped_gemm_a4, (P, P, P, P, P, 16, 4, 64, 128, P, NUL))
+    c = _caller(lib.w4a8_grouped_gemm_a4, (P, P, P, P, P, 16, 4, 64, 128, P, NUL, 0, NUL))
     assert c(a5=-1) == SHAPE and c(a6=0) == SHAPE and c(a6=2049) == SHAPE and c(a7=48) == SHAPE and c(a8=64) == SHAPE
     assert all(c(**{f"a{i}": NUL}) == NULL for i in (0, 1, 2, 3, 4, 9))
     assert all(c(**{f"a{i}": P8}) == ALIGN for i in (0, 2, 9)) and all(c(**{f"a{i}": P2}) == ALIGN for i in (1, 3, 4))

@@ -165,7 +165,9 @@ def _product(gpu_lib, counts, N, K, A, SA, B, SB, eps, extra=2):
 
 
 COUNTS = [([1], 32, 128), ([5, 0, 3], 64, 256), ([64, 1, 63, 65], 128, 640), ([130, 0, 257, 31], 288, 384),
-          ([16] * 12, 256, 512), ([300, 700], 544, 1024), ([3, 1, 4] * 30, 64, 128), ([128, 127, 129], 96, 3584)]
+          ([16] * 12, 256, 512), ([300, 700], 544, 1024), ([3, 1, 4] * 30, 64, 128), ([128, 127, 129], 96, 3584),
+          # long sums over few tiles, in slices
+          ([5, 0, 3], 64, 8192), ([40, 2], 96, 4224), ([1], 32, 2048)]
 
 
 @pytest.mark.parametrize("counts,N,K", COUNTS)

@@ -47,9 +47,20 @@ CASES = [
     ([1], 1, 1), ([3, 0, 5], 7, 5), ([40, 33], 33, 31), ([129, 1], 130, 257), ([20, 200], 255, 64), ([65], 64, 129),
     ([1] * 100, 12, 10),
 ]
+# long sums over few tiles, taken in slices (of K, of N or of the rows); ends inside and at the start of a slice
+LONG = [
+    ([3, 0, 7], 72, 5000), ([2], 128, 5969), ([40, 1], 4352, 64), ([9, 0, 60], 4097, 33), ([6000, 0, 30], 40, 24),
+    ([5, 5000], 31, 17), ([1, 1], 16, 1024), ([30, 0], 1024, 1024), ([513, 1023, 0, 2048], 64, 8),
+]
 
 
-@pytest.mark.parametrize("counts,N,K", CASES)
+def test_long_sums_are_sliced(gpu_lib):
+    need = gpu_lib.load().w4a8_grouped_gemm_workspace_bytes
+    for counts, N, K in LONG:
+        assert any(need(product, sum(counts), len(counts), N, K) for product in (0, 1, 2))
+
+
+@pytest.mark.parametrize("counts,N,K", CASES + LONG)
 def test_forward_and_gradients(gpu_lib, counts, N, K):
     R, E, extra = sum(counts), len(counts), 3
     A, Af = _draw(N + K, R + extra, K)
@@ -130,6 +141,61 @@ def test_bad_offsets_write_nothing(gpu_lib, bad):
     gpu_lib.grouped_gemm_dgrad(dC, W, off, out=o[1])
     gpu_lib.grouped_gemm_wgrad(dC, A, off, out=o[2])
     assert all((t == 7.0).all() for t in o)
+
+
+@pytest.mark.parametrize("bad", [[1, 4, 8], [0, 5, 4], [0, 4, 9], [-1, 4, 8]])
+def test_bad_offsets_write_nothing_in_slices(gpu_lib, bad):
+    off = torch.tensor(bad, dtype=torch.int32).cuda()
+    A, W, V, dC = (_dev(_draw(i, *s)[0]) for i, s in enumerate([(8, 1024), (2, 24, 1024), (2, 1024, 16), (8, 1024)]))
+    o = [torch.full(s, 7.0, dtype=torch.bfloat16, device="cuda") for s in ((8, 24), (8, 16))]
+    gpu_lib.grouped_gemm_bf16(A, W, off, out=o[0])
+    gpu_lib.grouped_gemm_dgrad(dC, V, off, out=o[1])
+    off = (off * 256).contiguous()
+    A, dC = (_dev(_draw(i, *s)[0]) for i, s in enumerate([(2048, 16), (2048, 24)]))
+    o.append(torch.full((2, 24, 16), 7.0, dtype=torch.bfloat16, device="cuda"))
+    gpu_lib.grouped_gemm_wgrad(dC, A, off, out=o[2])
+    assert all((t == 7.0).all() for t in o)
+
+
+def test_without_a_workspace(gpu_lib):
+    """NULL: the sum in one piece; the same within the sums' bound."""
+    lib, R, E, N, K = gpu_lib.load(), 10, 3, 72, 5000
+    (A, Af), (W, Wf) = _draw(1, R, K), _draw(2, E, N, K)
+    off, Ad, Wd = _off([3, 0, 7]), _dev(A), _dev(W)
+    out = torch.empty((R, N), dtype=torch.bfloat16, device="cuda")
+    assert lib.w4a8_grouped_gemm_bf16(Ad.data_ptr(), Wd.data_ptr(), off.data_ptr(), R, E, N, K, out.data_ptr(), None, 0,
+                                      torch.cuda.current_stream().cuda_stream) == 0
+    offs = off.cpu().numpy()
+    _check(out, grouped.forward_f64(Af, Wf, offs), grouped.forward_f64(Af, Wf, offs, absolute=True), K)
+
+
+def test_slices_on_two_streams_and_in_graphs(gpu_lib):
+    """Calls that may run at a time have workspaces of their own; replays give the eager results."""
+    off = _off([3, 0, 7])
+    A, W = [_dev(_draw(i, 10, 5000)[0]) for i in range(2)], _dev(_draw(7, 3, 72, 5000)[0])
+    want = [gpu_lib.grouped_gemm_bf16(a, W, off) for a in A]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in A]
+    got = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(gpu_lib.grouped_gemm_bf16(A[i], W, off))
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want[i]) for i in range(2) for g in got[i])
+    graphs, outs = [], []
+    for a in A:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(gpu_lib.grouped_gemm_bf16(a, W, off))
+    for _ in range(3):
+        for o in outs:
+            o.zero_()
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want))
+        assert torch.equal(gpu_lib.grouped_gemm_bf16(A[0], W, off), want[0])
 
 
 def test_many_experts(gpu_lib):
