@@ -8,10 +8,13 @@
 // the exact quotients.  MX divides by powers of two, which is exact.  NV's
 // quotients meet the grids' midpoints exactly when x and the amax share their
 // mantissas, and come as near as 2^-33 to them otherwise (x has 8 significant
-// bits, s 4, gs 24, a midpoint 3): both are told apart in 64 bits.
+// bits, s 4, gs 24, a midpoint 3): both are told apart exactly.
 //
-// A stream: a thread holds 16 columns, i.e. an NVFP4 group, two threads an MX
-// group.
+// Streams: a thread holds 16 columns, i.e. an NVFP4 group, two threads an MX
+// group.  Bound by HBM, 264 M weights: the experts' amax 91 us (5.8 TB/s), NVFP4
+// from it 120 (5.6), back 112 (6.0).  Tried: the weights read the second time past
+// the caches, 4% slower from 16 experts of 4096 x 4096 on; from the end, where the
+// amax pass left off, 3%.
 #include "swiglu.h"
 #include "w4a8_launch.h"
 
@@ -29,6 +32,7 @@ typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 
 constexpr int Q_THREADS = 256;
 constexpr int AMAX_UNROLL = 4;
+constexpr int64_t INFINITY_CACHE = 256 << 20;   // bytes
 constexpr float kScaleFloor = 7.888609052210118e-31f;  // 2^-100
 
 struct Cols { v4u lo, hi; };   // 16 bf16 columns
@@ -156,33 +160,20 @@ expert_amax_kernel(const uint16_t* __restrict__ x, int64_t units, int parts, int
   if (threadIdx.x == 0) partials[b] = m;
 }
 
-// v rounded to a multiple of u (a power of two), halves to even; |v| < 2^50 u.
-__device__ __forceinline__ double round_to(double v, double u) {
-  const double c = 6755399441055744.0 * u;   // 1.5 * 2^52
-  return (v + c) - c;
-}
-
-// The E2M1 code of |x| / t, t exact: the quotient in 64 bits is within 2^-51 of
-// the true one; a true midpoint is a multiple of 2^-40 and is restored by rounding
-// to one, everything else is 2^-33 off it.
-__device__ __forceinline__ uint32_t e2m1_exact(float x, double t) {
-  const double v = round_to(fabs((double)x) / t, 0x1p-40);
-  // the grid: steps of 1/2 up to 2, 1 up to 4, 2 up to 6
-  const float y = fminf((float)round_to(v, v < 2.0 ? 0.5 : v < 4.0 ? 1.0 : 2.0), 6.0f);
-  return (uint32_t)(y < 2.0f ? y * 2.0f : y < 4.0f ? y + 2.0f : fmaf(y, 0.5f, 4.0f));
-}
-// E4M3 of r in [0, 448 (1 + 2^-24)], exactly: steps of 2^(floor(log2 r) - 3), of 2^-9
-// below 2^-6.
-__device__ __forceinline__ float e4m3_exact(double r) {
-  int ex = r > 0.0 ? __builtin_amdgcn_frexp_exp(r) - 1 : -6;
-  ex = ex < -6 ? -6 : ex;
-  return (float)round_to(r, ldexp(1.0, ex - 3));
+// Which of two neighbours of a grid, codes k and k + 1 and values v[0] < v[1], the
+// quotient a / t goes to, a and t positive: a against the midpoint times t.  The
+// midpoint's product with what `scale` holds of t is exact (at most 7 bits), and the
+// fma rounds only the difference, whose sign it keeps.
+__device__ __forceinline__ uint32_t nearer(uint32_t k, v2f v, float scale, float t, float a) {
+  const float over = fmaf((v[0] + v[1]) * 0.5f * scale, -t, a);
+  return k + (over > 0.0f || (over == 0.0f && (k & 1)));
 }
 
 // Quotients are taken in fp32, within 2^-21 of the true ones, and rounded once
 // with 2^-20 less and once with 2^-20 more of their size; only where the two differ
 // does the exact quotient decide (in about one element of a thousand: x and the
-// amax share their mantissas).  All in 64 bits: 250 us for 264 M weights.
+// amax share their mantissas).  All in 64 bits: 250 us for 264 M weights; these
+// alone by division in 64 bits: 153, by nearer(): 120.
 __global__ void __launch_bounds__(Q_THREADS)
 quant_nv_kernel(const uint16_t* __restrict__ x, int64_t units, int64_t per_expert, int64_t b0, int parts,
                 const uint32_t* __restrict__ partials, uint8_t* __restrict__ B, uint8_t* __restrict__ SB,
@@ -209,8 +200,8 @@ quant_nv_kernel(const uint16_t* __restrict__ x, int64_t units, int64_t per_exper
     const float a = __uint_as_float(am), r = a * ig * (1.0f / 6.0f);
     code = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(r * LESS, r * MORE, 0, false);
     if ((code & 0xff) != (code >> 8 & 0xff)) {
-      const float s = e4m3_exact((double)a / (6.0 * (double)g));
-      code = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(s, 0.0f, 0, false);   // keeps a number of its grid
+      code &= 0xff;   // the lower one
+      code = nearer(code, __builtin_amdgcn_cvt_pk_f32_fp8((int)(code | (code + 1) << 8), false), 6.0f, g, a);
     }
     code &= 0xff;
     const float s = __builtin_amdgcn_cvt_f32_fp8((int)code, 0);
@@ -234,8 +225,9 @@ quant_nv_kernel(const uint16_t* __restrict__ x, int64_t units, int64_t per_exper
         const int at = (__ffs((int)todo) - 1) & ~3, j = at >> 2;   // element j of the 8
         const uint32_t pair = j < 4 ? (j < 2 ? cols[0] : cols[1]) : (j < 6 ? cols[2] : cols[3]);
         const float xf = __uint_as_float(j & 1 ? pair & 0xffff0000u : pair << 16);
-        const uint32_t k = e2m1_exact(xf, (double)s * (double)g) | ((__float_as_uint(xf) >> 28) & 8u);
-        lo = (lo & ~(15u << at)) | (k << at);
+        const uint32_t k = lo >> at & 7;   // the lower one, its sign apart
+        const v2f v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(k | (k + 1) << 4, 1.0f, 0);
+        lo += (nearer(k, v, s, g, fabsf(xf)) - k) << at;
         todo &= ~(15u << at);
       }
       q[h] = lo;
@@ -246,8 +238,11 @@ quant_nv_kernel(const uint16_t* __restrict__ x, int64_t units, int64_t per_exper
 }
 
 // Codes to bf16: a thread decodes 8 columns.  value = bf16((code * s) gs), code
-// * s exact in fp32.
-template <bool NV>
+// * s exact in fp32.  PAST: the output is larger than the Infinity Cache and goes
+// round it.  From MXFP4, then with a product that reads the weights, us, through
+// it | round it: 201 MB 37, 96 | 49, 114; 268 MB 67, 131 | 64, 129; 1074 MB 257,
+// 456 | 253, 429.
+template <bool NV, bool PAST>
 __global__ void __launch_bounds__(Q_THREADS)
 dequant_kernel(const uint8_t* __restrict__ B, const uint8_t* __restrict__ SB, const float* __restrict__ gs,
                int64_t units, int64_t per_expert, int64_t b0, uint16_t* __restrict__ out) {
@@ -255,7 +250,8 @@ dequant_kernel(const uint8_t* __restrict__ B, const uint8_t* __restrict__ SB, co
   const int64_t u = (b - e * per_expert) * Q_THREADS + threadIdx.x;
   if (u >= units) return;
   const int64_t i = e * units + u;
-  const uint32_t q = *reinterpret_cast<const uint32_t*>(B + i * 4);
+  const uint32_t* p = reinterpret_cast<const uint32_t*>(B + i * 4);
+  const uint32_t q = PAST ? __builtin_nontemporal_load(p) : *p;
   const float g = gs ? gs[e] : 1.0f;
   const uint32_t sc = SB[NV ? i >> 1 : i >> 2];
   const float s = NV ? __builtin_amdgcn_cvt_f32_fp8((int)sc, 0) : 1.0f;
@@ -275,7 +271,8 @@ dequant_kernel(const uint8_t* __restrict__ B, const uint8_t* __restrict__ SB, co
   W4A8_DEQ(2)
   W4A8_DEQ(3)
 #undef W4A8_DEQ
-  *reinterpret_cast<v4u*>(out + i * 8) = o;
+  if (PAST) __builtin_nontemporal_store(o, reinterpret_cast<v4u*>(out + i * 8));
+  else *reinterpret_cast<v4u*>(out + i * 8) = o;
 }
 
 // Parts of an expert's amax: enough workgroups for the chip over all experts,
@@ -315,13 +312,11 @@ hipError_t launch_quant_fp4(const uint16_t* x, bool nv, int E, int N, int K, uin
 hipError_t launch_dequant_fp4(const uint8_t* B, const uint8_t* SB, bool nv, const float* gs, int E, int N, int K,
                               uint16_t* out, hipStream_t stream) {
   const int64_t units = (int64_t)N * (K / 8), per = (units + Q_THREADS - 1) / Q_THREADS;
+  const bool past = units * E * 16 > INFINITY_CACHE;
+  const auto kernel = nv ? past ? dequant_kernel<true, true> : dequant_kernel<true, false>
+                         : past ? dequant_kernel<false, true> : dequant_kernel<false, false>;
   return in_launches(per * E, Q_THREADS, [&](int64_t b, int64_t n) {
-    if (nv)
-      hipLaunchKernelGGL(dequant_kernel<true>, dim3((unsigned)n), dim3(Q_THREADS), 0, stream, B, SB, gs, units, per, b,
-                         out);
-    else
-      hipLaunchKernelGGL(dequant_kernel<false>, dim3((unsigned)n), dim3(Q_THREADS), 0, stream, B, SB, gs, units, per,
-                         b, out);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)n), dim3(Q_THREADS), 0, stream, B, SB, gs, units, per, b, out);
   });
 }
 

