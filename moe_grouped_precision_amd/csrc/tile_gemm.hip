@@ -19,9 +19,12 @@
 // What bounds them (32 experts 4096 x 6144, unevenly filled).  The forward product
 // of 9216 rows, 575 us, 1.8 GB: its loads.  They alone take as long; a CU has 80 lines
 // on their way at a mean latency of 505 cycles, 6.2 GB come from L2 and 2.1 of them
-// from memory, the matrix cores are 27% busy at 2.26 GHz.  The gradients, 1.65 TFLOP
-// in 1529 us and 3.3 in 2816, and 4 by 4 bits, 6.6 in 1934: power, the matrix cores
-// 63% busy at 1.45 to 1.73 GHz.  Few rows: the weights' bytes, 4.9 TB/s.
+// from memory, the matrix cores are 0.4 busy.  The row gradient, 1.65 TFLOP in 1517 us,
+// and the weights', 3.3 in 2839 (2560 without its 1.6 GB of stores): the matrix cores
+// 0.50 and 0.58 busy at 2.0 and 1.9 GHz, where normal values alone keep them at 2070
+// TFLOP/s; half the misses in L2 do not change it.  4 by 4 bits, 6.6 in 1875: LDS, whose
+// reads take as long as the matrix instructions, and the stores.  Few rows: the
+// weights' bytes, 4.9 TB/s.
 // Tried on the forward product and the weights' gradient, us: loads in one burst 728
 // and 5020; steps of 64 bytes (half lines) in 4 or 5 stages 735, 2774; 128 x 256 in
 // two stages 751, 256 x 256 in two 637, 192 x 192 in three 620 (605 on that day);
@@ -284,6 +287,76 @@ __device__ __forceinline__ void put(const TileArgs& a, const Place& p, const Ope
 #pragma unroll
       for (int c = 0; c < 4; ++c)
         if (c < n) o[c] = __builtin_bit_cast(uint16_t, (__bf16)v[c]);
+  }
+}
+
+// Lanes 8 .. 15 of every 16 of a with lanes 0 .. 7 of b.
+__device__ __forceinline__ void swap_halves(v4i& a, v4i& b) {
+  const v4i t = a;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    a[c] = __builtin_amdgcn_update_dpp(a[c], b[c], 0x128, 0xf, 0xc, false);   // row_ror:8
+    b[c] = __builtin_amdgcn_update_dpp(b[c], t[c], 0x128, 0xf, 0x3, false);
+  }
+}
+
+// The lane's results of a row block, MX column blocks from x on, to memory.  In the
+// instruction's layout a store has 32 (bf16) or 64 bytes of each of 16 rows, and the
+// tiles of a round all store at a time, while nothing else runs on their CUs: lanes
+// exchange values until a store has whole lines, and these pass the L2 cache that
+// the next tiles' operands lie in.  131072 rows, 4 by 4 bits, 1990 us, so 1909 and
+// past the cache 1875 (without any store 1670); weights' gradient 2879, 2866, 2839;
+// row gradient 1564, 1528, 1517; forward 597, 590, 579.  What reads the output next
+// takes 5% longer to 16% less.
+template <int MODE, int MX, typename OUT>
+__device__ __forceinline__ void put_block(const TileArgs& a, const Place& p, const Operands<MODE>& op, int y, int x,
+                                          const v4f (&acc)[MX]) {
+  const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
+  if (a.wide < 2 || (sizeof(OUT) == 2 && MODE == WEIGHTS && a.accumulate)) {
+#pragma unroll
+    for (int j = 0; j < MX; ++j) put<MODE, OUT>(a, p, op, y + i, x + 16 * j + 4 * q, acc[j]);
+    return;
+  }
+  constexpr int PER = 16 / sizeof(OUT), PAIRS = MX * 16 / (4 * PER) / 2;   // values of a store, pairs of stores
+  auto store = [&](int row, int col, v4i v) {
+    if (row >= p.ny || col >= p.nx) return;
+    OUT* o = static_cast<OUT*>(a.out) + op.out0 +
+             (MODE == WEIGHTS ? (size_t)p.e * a.N + p.y0 + row : (size_t)(p.r0 + p.y0 + row)) * op.width + p.x0 + col;
+    v4i* const at = reinterpret_cast<v4i*>(o);
+    if (sizeof(OUT) == 4 && MODE == WEIGHTS && a.accumulate)
+      v = __builtin_bit_cast(v4i, __builtin_bit_cast(v4f, v) + *reinterpret_cast<const v4f*>(o));
+    __builtin_nontemporal_store(v, at);
+  };
+  v4i v[MX * 16 / (4 * PER)];
+  if constexpr (sizeof(OUT) == 4) {
+#pragma unroll
+    for (int j = 0; j < MX; ++j) v[j] = __builtin_bit_cast(v4i, acc[j]);
+  } else {
+    // blocks 2 j and 2 j + 1: a lane gets 8 columns of one, 4 (q & 2) of block q & 1
+#pragma unroll
+    for (int j = 0; j < MX / 2; ++j)
+#pragma unroll
+      for (int d = 0; d < 2; ++d) {
+        const auto pack = [&](v4f f) {
+          return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f){f[2 * d], f[2 * d + 1]}, v2bf));
+        };
+        const auto r = __builtin_amdgcn_permlane16_swap(pack(acc[2 * j]), pack(acc[2 * j + 1]), false, false);
+        v[j][d] = (int)r[0];
+        v[j][2 + d] = (int)r[1];
+      }
+  }
+  // a store's columns of its first or only 64 bytes of a row
+  const int col = sizeof(OUT) == 4 ? x + 4 * q : x + 16 * (q & 1) + 4 * (q & 2);
+  if constexpr (PAIRS == 0) {
+    store(y + i, col, v[0]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < PAIRS; ++j) {
+      swap_halves(v[2 * j], v[2 * j + 1]);
+      const int at = col + (2 * j + (i >> 3)) * (4 * PER);
+      store(y + (i & 7), at, v[2 * j]);
+      store(y + 8 + (i & 7), at, v[2 * j + 1]);
+    }
   }
 }
 
@@ -632,9 +705,7 @@ struct Direct {
     if (MODE == WEIGHTS && a.accumulate && steps == 0) return;
 #pragma unroll
     for (int i = 0; i < MY; ++i)
-#pragma unroll
-      for (int j = 0; j < MX; ++j)
-        put<MODE, OUT>(a, p, op, (i * WY + wy) * 16 + (lane & 15), (wx * MX + j) * 16 + 4 * (lane >> 4), acc[i][j]);
+      put_block<MODE, MX, OUT>(a, p, op, (i * WY + wy) * 16, wx * MX * 16, acc[i]);
   }
 };
 
@@ -713,7 +784,10 @@ join_kernel(TileArgs a, const float* __restrict__ parts) {
 bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 template <typename OUT>
-bool wide_out(const TileArgs& a, int width) { return width % 4 == 0 && aligned_to(a.out, 4 * sizeof(OUT)); }
+int wide_out(const TileArgs& a, int width) {
+  if (width % (16 / sizeof(OUT)) == 0 && aligned_to(a.out, 16)) return 2;
+  return width % 4 == 0 && aligned_to(a.out, 4 * sizeof(OUT));
+}
 
 // Where a product has fewer tiles than the chip has CUs and a long sum, the sum is
 // cut into slices (parts of fp32 in the workspace, added in order): 3 rows, 128 x
