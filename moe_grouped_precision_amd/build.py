@@ -14,6 +14,7 @@ import shutil
 import subprocess
 import sys
 import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -27,6 +28,7 @@ SOURCES = ["api.cpp", "prep.hip", "gemm.hip", "quant.hip", "combine.hip", "a16.h
 PROBE_LIB = os.path.join(HERE, "libw4a8_probe.so")
 PROBE_SOURCES = ["probe.hip"]
 ARCH = "gfx950"
+JOBS = min(8, os.cpu_count() or 1)   # compilers at a time
 
 
 def hipcc() -> str:
@@ -65,7 +67,8 @@ def check_device_asm(cc: str, tmp: str, verbose: bool = False) -> None:
     check on it; raise if it reports anything."""
     from . import asmcheck
 
-    for src, lds in ASM_CHECKED.items():
+    def check(item):
+        src, lds = item
         path = os.path.join(CSRC, src)
         asm = os.path.join(tmp, src.replace(".", "_") + ".s")
         cmd = [cc, "-x", "hip", *compile_flags(), "--cuda-device-only", "-S", path, "-o", asm]
@@ -79,10 +82,12 @@ def check_device_asm(cc: str, tmp: str, verbose: bool = False) -> None:
             raise RuntimeError(f"device assembly of {src} fails the load/wait check:\n" +
                                "\n".join(findings[:20]))
 
+    with ThreadPoolExecutor(JOBS) as pool:
+        list(pool.map(check, ASM_CHECKED.items()))
+
 
 def _link(cc, tmp, sources, out, verbose, debug):
-    objs = []
-    for src in sources:
+    def compile_one(src):
         path = os.path.join(CSRC, src)
         obj = os.path.join(tmp, src.replace(".", "_") + ".o")
         cmd = [cc, "-x", "hip", *compile_flags(debug), "-c", path, "-o", obj]
@@ -91,7 +96,10 @@ def _link(cc, tmp, sources, out, verbose, debug):
         res = subprocess.run(cmd, capture_output=True, text=True)
         if res.returncode != 0:
             raise RuntimeError(f"hipcc failed on {src}:\n{res.stderr}")
-        objs.append(obj)
+        return obj
+
+    with ThreadPoolExecutor(JOBS) as pool:
+        objs = list(pool.map(compile_one, sources))
     tmp_lib = os.path.join(tmp, os.path.basename(out))
     cmd = [cc, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp_lib]
     if verbose:
