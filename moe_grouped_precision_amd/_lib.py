@@ -882,7 +882,7 @@ def grouped_gemm_wgrad(dC: torch.Tensor, A: torch.Tensor, expert_offsets: torch.
         if accumulate:
             raise ValueError("accumulate adds to a given out")
         out = torch.empty((E, N, K), dtype=torch.float32, device=dC.device)
-    if out.dtype is torch.float32:
+    if getattr(out, "dtype", None) is torch.float32:
         _need(out, "out", torch.float32, E * N * K)
     else:
         _bf16(out, "out", E * N * K)
@@ -937,6 +937,8 @@ def quantize_fp4(w: torch.Tensor, fmt: int, B: Optional[torch.Tensor] = None, SB
         _check("w4a8_quantize_fp4", lib.w4a8_quantize_fp4(
             _ptr(w), int(fmt), E, N, K, _ptr(B), _ptr(SB), _ptr(expert_scales), _ptr(workspace),
             0 if workspace is None else workspace.numel(), _stream()))
+    elif expert_scales is not None:
+        expert_scales.fill_(1.0)   # of experts without weights, as of those of zeros
     return B, SB, expert_scales
 
 

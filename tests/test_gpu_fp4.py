@@ -225,6 +225,7 @@ def test_refusals_and_empty(gpu_lib):
     for fmt in (MX, NV):
         B, SB, g = gpu_lib.quantize_fp4(e, fmt)
         assert B.shape == (0, 32) and gpu_lib.dequantize_fp4(B, SB, fmt, g).shape == (0, 64)
+        assert g is None if fmt == MX else (g == 1).all()
     A, SA = gpu_lib.quantize_gather_fp4(e, torch.empty(0, dtype=torch.int32, device="cuda"), 2, 3)
     assert A.shape == (3, 32) and (A == 0).all() and (SA == 0).all()
     Bw, SBw, _ = gpu_lib.quantize_fp4(torch.zeros((2, 32, 128), dtype=torch.bfloat16, device="cuda"), MX)

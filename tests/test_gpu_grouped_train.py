@@ -45,7 +45,7 @@ CASES = [
     ([1700, 0, 900], 264, 200), ([2000], 520, 328), ([801, 815], 72, 456),
     # not whole 16-byte pieces
     ([1], 1, 1), ([3, 0, 5], 7, 5), ([40, 33], 33, 31), ([129, 1], 130, 257), ([20, 200], 255, 64), ([65], 64, 129),
-    ([1] * 100, 12, 10),
+    ([1] * 100, 12, 10), ([40, 3], 132, 64), ([200, 90], 388, 72),
 ]
 # long sums over few tiles, taken in slices (of K, of N or of the rows); ends inside and at the start of a slice
 LONG = [
@@ -249,6 +249,7 @@ def test_empty_and_refusals(gpu_lib):
         with pytest.raises(ValueError):
             call()
     for call in (lambda: gpu_lib.grouped_gemm_bf16(A.float(), W, z), lambda: gpu_lib.grouped_gemm_bf16(A, W, z.long()),
+                 lambda: gpu_lib.grouped_gemm_wgrad(A, A, z, out=[0.0]),
                  lambda: gpu_lib.grouped_gemm_wgrad(A, A, z, out=torch.empty((2, 16, 16), dtype=torch.float16, device="cuda"))):
         with pytest.raises(TypeError):
             call()
