@@ -13,10 +13,11 @@
 // from 2^64 on), and inv is applied in two factors, so that rows of the
 // largest and the smallest values come out like any other.
 //
-// Bound by HBM: 16384 x 6144 with the residual, 805 MB, 138 us (5.8 TB/s; stores
-// past the caches 135, but the next kernel reads what they store); the gradient of
-// 16383 x 6144 with dres, 805 MB, 184 and 5 for dw (4.3).  64 rows to 8 bits: 4.1 us,
-// a launch and a trip to memory.
+// Bound by HBM: 16384 x 6144 with the residual, 805 MB, 136 us (5.9 TB/s; stores in
+// the caches' way 141, 101 MB of output 74 in place of 58; what then reads the
+// output takes within 2% of the same); the gradient of 16383 x 6144 with dres, 805
+// MB, 145 and 5 for dw (5.5; in the caches' way 153, with a division by K for each
+// sum 182).  64 rows to 8 bits: 4.1 us, a launch and a trip to memory.
 #include "swiglu.h"
 #include "w4a8_launch.h"
 
@@ -58,7 +59,7 @@ __device__ __forceinline__ v4u load_chunk(const uint16_t* p, int n) {
 template <bool VEC>
 __device__ __forceinline__ void store_chunk(uint16_t* p, v4u a, int n) {
   if (VEC) {
-    *reinterpret_cast<v4u*>(p) = a;
+    __builtin_nontemporal_store(a, reinterpret_cast<v4u*>(p));
   } else if (n >= 8) {
     __builtin_memcpy(p, &a, 16);
   } else {
@@ -213,6 +214,7 @@ rms_norm_kernel(NormArgs a, int rows_per, int64_t row0) {
   const RowPlace r = place_of(rows_per, b, a.T - row0);
   if (!r.live) return;
   const size_t t = (size_t)(row0 + r.t), base = t * a.K;
+  const double ik = 1.0 / a.K;
   float f[NCH][8];
   double ss[1] = {0.0};
 #pragma unroll
@@ -239,7 +241,7 @@ rms_norm_kernel(NormArgs a, int rows_per, int64_t row0) {
     for (int i = 0; i < 8; ++i) ss[0] = fma((double)f[j][i], (double)f[j][i], ss[0]);
   int turn = 0;
   row_sum<1>(ss, r.waves, sums, turn);
-  const Inv c = inv_sqrt(ss[0] / a.K + (double)a.eps);
+  const Inv c = inv_sqrt(ss[0] * ik + (double)a.eps);
   const int G = a.K >> 7;
 #pragma unroll
   for (int j = 0; j < NCH; ++j) {
@@ -265,6 +267,7 @@ rms_norm_long_kernel(NormArgs a, int64_t row0) {
   __shared__ double sums[2][1][NORM_WAVES];
   const size_t t = (size_t)(row0 + blockIdx.x), base = t * a.K;
   const int G = a.K >> 7;
+  const double ik = 1.0 / a.K;
   double ss[1] = {0.0};
   float f[8], g[8];
   for (int k = threadIdx.x * 8; k < a.K; k += blockDim.x * 8) {
@@ -284,7 +287,7 @@ rms_norm_long_kernel(NormArgs a, int64_t row0) {
   }
   int turn = 0;
   row_sum<1>(ss, blockDim.x >> 6, sums, turn);
-  const Inv c = inv_sqrt(ss[0] / a.K + (double)a.eps);
+  const Inv c = inv_sqrt(ss[0] * ik + (double)a.eps);
   for (int k = threadIdx.x * 8; k < a.K; k += blockDim.x * 8) {
     const int n = a.K - k;
     float w[8], y[8];
@@ -314,6 +317,7 @@ __global__ void __launch_bounds__(64 * GRAD_WAVES)
 rms_norm_backward_kernel(NormGradArgs a) {
   __shared__ double sums[2][2][NORM_WAVES];
   const int waves = blockDim.x >> 6;
+  const double ik = 1.0 / a.K;
   float w[NCH][8], dw[NCH][8];
   v4u hv[NCH], dv[NCH], rv[NCH];
   auto load_row = [&](int64_t t) {
@@ -360,9 +364,9 @@ rms_norm_backward_kernel(NormGradArgs a) {
       }
     }
     row_sum<2>(s, waves, sums, turn);
-    const Inv c = inv_sqrt(s[0] / a.K + (double)a.eps);
+    const Inv c = inv_sqrt(s[0] * ik + (double)a.eps);
     // sum(g xh) / K
-    const float m = (float)(s[1] * (double)c.c1 * (double)c.c2 / a.K);
+    const float m = (float)(s[1] * (double)c.c1 * (double)c.c2 * ik);
 #pragma unroll
     for (int j = 0; j < NCH; ++j) {
       const int k = (threadIdx.x + j * blockDim.x) * 8, n = a.K - k;
@@ -397,6 +401,7 @@ __global__ void __launch_bounds__(64 * NORM_WAVES)
 rms_norm_backward_long_kernel(NormGradArgs a) {
   __shared__ double sums[2][2][NORM_WAVES];
   float* part = a.partials + (size_t)blockIdx.x * a.K;
+  const double ik = 1.0 / a.K;
   int turn = 0;
   for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
     const size_t base = (size_t)t * a.K;
@@ -414,8 +419,8 @@ rms_norm_backward_long_kernel(NormGradArgs a) {
       }
     }
     row_sum<2>(s, blockDim.x >> 6, sums, turn);
-    const Inv c = inv_sqrt(s[0] / a.K + (double)a.eps);
-    const float m = (float)(s[1] * (double)c.c1 * (double)c.c2 / a.K);
+    const Inv c = inv_sqrt(s[0] * ik + (double)a.eps);
+    const float m = (float)(s[1] * (double)c.c1 * (double)c.c2 * ik);
     for (int k = threadIdx.x * 8; k < a.K; k += blockDim.x * 8) {
       const int n = a.K - k;
       float f[8], d[8], w[8], r[8] = {0, 0, 0, 0, 0, 0, 0, 0}, o[8];
