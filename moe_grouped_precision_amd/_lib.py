@@ -4,6 +4,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from array import array
 from typing import Optional
 
 import torch
@@ -1025,7 +1026,7 @@ _GRAD_TYPES = {torch.float32: 0, torch.bfloat16: 1}
 
 def _grad_list(tensors, name, like=None):
     """(pointers, elements, types) of a list of tensors.  Each property of all at a time: this is most of a small
-    call's time (40 tensors and their outputs: 35 us a call, 42 with one tensor tested after the other)."""
+    call's time (40 tensors and their outputs: 29 us a call, 36 with one tensor tested after the other)."""
     dev = _current_device()
     if not all(isinstance(t, _Tensor) for t in tensors):
         raise TypeError(f"{name}s must be torch tensors")
@@ -1057,14 +1058,16 @@ def _grads(tensors, outs, max_norm, eps, norm, workspace):
     if norm is None:
         norm = torch.empty(1, dtype=torch.float32, device=torch.device("cuda", _current_device()))
     _need(norm, "norm", torch.float32, 1)
-    numel = (ctypes.c_int64 * n)(*found[1])
+    # array.array: a third of the time of a ctypes array (40 tensors: 32 us a call with those)
+    ptrs, numel, kinds = array("Q", found[0]), array("q", found[1]), array("i", found[2])
+    optrs = None if outs is None else array("Q", optrs)
+    at_numel = numel.buffer_info()[0]
     if workspace is None:
-        workspace = torch.empty(lib.w4a8_clip_grads_bytes(numel, n), dtype=torch.uint8, device=norm.device)
+        workspace = torch.empty(lib.w4a8_clip_grads_bytes(at_numel, n), dtype=torch.uint8, device=norm.device)
     _need(workspace, "workspace", torch.uint8)
     _here(norm, workspace)
-    array = ctypes.c_void_p * n
     _check("w4a8_clip_grads", lib.w4a8_clip_grads(
-        array(*found[0]), None if outs is None else array(*optrs), numel, (ctypes.c_int * n)(*found[2]), n,
+        ptrs.buffer_info()[0], None if outs is None else optrs.buffer_info()[0], at_numel, kinds.buffer_info()[0], n,
         float(max_norm), float(eps), _ptr(workspace), workspace.numel(), _ptr(norm), _stream()))
     return norm
 

@@ -14,7 +14,7 @@
 // Bound by HBM: 1057 MB of gradients, norm 173 us (6.1 TB/s), clipping 341 (6.2).
 // 1024 workgroups, four waves to a SIMD (2048: 595 us for both in place of 564, 768:
 // 566, 512: 634; twice the loads of a thread: 580).  Small lists: 40 tensors of up
-// to 300000 elements 4.6 and 6.4 us, their call 31 by the host's work.
+// to 300000 elements 4.6 and 6.4 us, their call 29 by the host's work.
 #include "w4a8_launch.h"
 
 #include <hip/hip_runtime.h>
