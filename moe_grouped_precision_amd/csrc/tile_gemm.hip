@@ -366,14 +366,13 @@ __device__ __forceinline__ v4f mfma_bf16(v4i x, v4i y, v4f acc) {
 
 // ---------------------------------------------------------------------------
 // Rows that are no whole 16-byte chunks at 16-byte addresses: through registers,
-// 128 x 128 tiles, steps of 32 z, two of them in LDS and two on their way.  Bound
-// by the loads at 2-byte addresses and the writes to LDS: 200 to 250 TFLOP/s
-// (weights' gradient of 11365 rows, 45 experts, 4440 x 2165: 980 us).
+// 128 x 128 tiles, steps of 32 KS z, two of them in LDS and one on its way (a second
+// one changes nothing).  Bound by the loads at 2-byte addresses and the writes to LDS.
 // ---------------------------------------------------------------------------
-template <int MODE, typename OUT>
+template <int MODE, int KS_, typename OUT>
 struct General {
-  static constexpr int TY = 128, TX = 128, KS = 1, NW = 4, THREADS = 256, M = 4, NI = TY / 16 / NW;
-  static constexpr int STAGE = (TY + TX) * 64, LDS = 2 * STAGE, PER_SIMD = 2;
+  static constexpr int TY = 128, TX = 128, KS = KS_, NW = 4, THREADS = 256, M = 4, NI = TY * KS / 16 / NW, ZSTEP = 32 * KS;
+  static constexpr int STAGE = (TY + TX) * 64 * KS, LDS = 2 * STAGE, PER_SIMD = 2;
 
   static __device__ __forceinline__ void run(const TileArgs& a, int64_t b, uint32_t lds) {
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
@@ -381,7 +380,7 @@ struct General {
     if (!find_tile<MODE, TY, TX>(a, b, p)) return;
     const Operands<MODE> op(a, p);
     constexpr bool YT = Operands<MODE>::YT, XT = Operands<MODE>::XT;
-    const int steps = (op.zn + 31) / 32;
+    const int steps = (op.zn + ZSTEP - 1) / ZSTEP;
     v4f acc[M][M];
 #pragma unroll
     for (int i = 0; i < M; ++i)
@@ -411,65 +410,62 @@ struct General {
         left[i] = op.zn - chunk * 8;
       }
     }
-    const size_t ystep = YT ? (size_t)32 * op.ybytes : 64, xstep = XT ? (size_t)32 * op.xbytes : 64;
-    // two steps ahead in registers, one in LDS: a step takes as long as the way to
-    // memory where there are few tiles
-    v4i reg[2][2 * NI];
+    const size_t ystep = YT ? (size_t)ZSTEP * op.ybytes : 64 * KS, xstep = XT ? (size_t)ZSTEP * op.xbytes : 64 * KS;
+    v4i reg[2 * NI];
     const bool few_y = op.ybytes < 16, few_x = op.xbytes < 16;
     // values of chunk i in step s
     auto values = [&](int i, int s) {
-      const int z = left[i] - 32 * s;
+      const int z = left[i] - ZSTEP * s;
       return (i < NI ? YT : XT) ? (z > 0 ? wide[i] : 0) : z;
     };
-    auto fetch = [&](int s, int to) {
+    auto fetch = [&](int s) {
 #pragma unroll
       for (int i = 0; i < 2 * NI; ++i) {
         const int n = values(i, s);
-        if (i < NI ? few_y : few_x) reg[to][i] = load_few(src[i], n);
-        else reg[to][i] = load_any(src[i], n);
+        if (i < NI ? few_y : few_x) reg[i] = load_few(src[i], n);
+        else reg[i] = load_any(src[i], n);
         src[i] += i < NI ? ystep : xstep;
       }
     };
     // which operands have such ends, in any step or in the last
     const bool end_y = !few_y && (YT ? (p.ny & 7) != 0 : (op.zn & 7) != 0);
     const bool end_x = !few_x && (XT ? (p.nx & 7) != 0 : (op.zn & 7) != 0);
-    auto fill = [&](int s, int from) {
+    auto fill = [&](int s, int to) {
 #pragma unroll
       for (int i = 0; i < 2 * NI; ++i) {
-        if ((i < NI ? end_y : end_x) && ((i < NI ? YT : XT) || s == steps - 1)) reg[from][i] = only(reg[from][i], values(i, s));
-        *(lds_v4i*)(uintptr_t)(lds + from * STAGE + (i / NI) * TY * 64 + (wave + NW * (i % NI)) * 1024 + lane * 16) =
-            reg[from][i];
+        if ((i < NI ? end_y : end_x) && ((i < NI ? YT : XT) || s == steps - 1)) reg[i] = only(reg[i], values(i, s));
+        *(lds_v4i*)(uintptr_t)(lds + to * STAGE + (i / NI) * TY * 64 * KS + (wave + NW * (i % NI)) * 1024 + lane * 16) =
+            reg[i];
       }
     };
     const int wy = wave >> 1, wx = wave & 1;
-    auto step = [&](int s, int at) {   // at = s & 1
-      if (s + 2 < steps) fetch(s + 2, at);
+    auto step = [&](int s, int at) {
+      if (s + 1 < steps) fetch(s + 1);
       const uint32_t stage = lds + at * STAGE;
-      v4i fy[M], fx[M];
 #pragma unroll
-      for (int i = 0; i < M; ++i) {
-        fy[i] = YT ? frag_cols<TY>(cols_base<TY>(lane), stage, wy * M + i, 0)
-                   : frag_rows<KS>(rows_base<KS>(stage, 0, lane), wy * M + i);
-        fx[i] = XT ? frag_cols<TX>(cols_base<TX>(lane), stage + TY * 64, wx * M + i, 0)
-                   : frag_rows<KS>(rows_base<KS>(stage + TY * 64, 0, lane), wx * M + i);
+      for (int h = 0; h < KS; ++h) {
+        v4i fy[M], fx[M];
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+          fy[i] = YT ? frag_cols<TY>(cols_base<TY>(lane), stage, wy * M + i, h)
+                     : frag_rows<KS>(rows_base<KS>(stage, h, lane), wy * M + i);
+          fx[i] = XT ? frag_cols<TX>(cols_base<TX>(lane), stage + TY * 64 * KS, wx * M + i, h)
+                     : frag_rows<KS>(rows_base<KS>(stage + TY * 64 * KS, h, lane), wx * M + i);
+        }
+#pragma unroll
+        for (int i = 0; i < M; ++i)
+#pragma unroll
+          for (int j = 0; j < M; ++j) acc[i][j] = mfma_bf16(fx[j], fy[i], acc[i][j]);
       }
-#pragma unroll
-      for (int i = 0; i < M; ++i)
-#pragma unroll
-        for (int j = 0; j < M; ++j) acc[i][j] = mfma_bf16(fx[j], fy[i], acc[i][j]);
       if (s + 1 < steps) fill(s + 1, at ^ 1);
       __syncthreads();
     };
     if (steps > 0) {
-      fetch(0, 0);
-      if (steps > 1) fetch(1, 1);
+      fetch(0);
       fill(0, 0);
       __syncthreads();
     }
-    for (int s = 0; s < steps; s += 2) {
-      step(s, 0);
-      if (s + 1 < steps) step(s + 1, 1);
-    }
+    for (int s = 0; s < steps; ++s) step(s, s & 1);
     if (MODE == WEIGHTS && a.accumulate && steps == 0) return;
 #pragma unroll
     for (int i = 0; i < M; ++i)
@@ -813,6 +809,19 @@ hipError_t launch_sliced(TileArgs a, void* work, hipStream_t stream, F launch_ti
   return hipGetLastError();
 }
 
+// Steps of 64 z where the forward product's operands lie along z, and for few rows,
+// which read most of what they load once; steps of 32, with three workgroups on a CU
+// in place of two, for the others.  us, 64 | 32: forward, 9216 rows, 32 experts 4096 x
+// 2047 387 | 422, 88 rows, 29 experts 2554 x 3266 117 | 130; row gradient, 88 rows, 29
+// experts 2553 x 1266 75 | 98, 97704 rows, 9 experts 838 x 401 219 | 205; weights'
+// gradient, 65536 rows, 8 experts 1447 x 1025 501 | 430.
+template <int MODE, typename OUT>
+hipError_t launch_odd(const TileArgs& a, hipStream_t stream) {
+  if constexpr (MODE != WEIGHTS)
+    if (MODE == FWD || a.R / a.E <= FEW_ROWS) return launch<MODE, General<MODE, 2, OUT>>(a, stream);
+  if constexpr (MODE != FWD) return launch<MODE, General<MODE, 1, OUT>>(a, stream);
+}
+
 // Tiles by the mean number of rows of an expert (all that the host knows).
 // 4096 x 6144, 32 experts, unevenly filled, us a call, forward | row gradient:
 //   rows        16          64          128         288          512          1024
@@ -826,12 +835,12 @@ hipError_t launch_sliced(TileArgs a, void* work, hipStream_t stream, F launch_ti
 // 288: 1133 / 1253, 1024: 2070 / 2282).
 template <int MODE, typename OUT>
 hipError_t launch_bf16(const TileArgs& a, hipStream_t stream) {
+  const int rows = a.R / a.E;
   // Whole chunks: along K of the forward product's rows, along both of the others.
   // A tile's offsets within an operand are 32 bits: 256 rows, or 64 of z, of 8 MB
   // at most.
   if (a.K % 8 || (MODE != FWD && a.N % 8) || !aligned_to(a.Y, 16) || !aligned_to(a.X, 16) || a.N > (1 << 22))
-    return launch<MODE, General<MODE, OUT>>(a, stream);
-  const int rows = a.R / a.E;
+    return launch_odd<MODE, OUT>(a, stream);
   if constexpr (MODE == FWD)
     if (rows <= FEW_ROWS) return launch<MODE, Direct<MODE, 64, 128, 1, 4, 3, OUT>>(a, stream);
   if constexpr (MODE != WEIGHTS)
@@ -851,6 +860,13 @@ hipError_t launch_four(const TileArgs& a, hipStream_t stream) {
 
 }  // namespace
 
+// Slices of a sum: as many as bring the workgroups to the number that the chip holds
+// at a time, none shorter than `least`, and none at all below `from`, where the join's
+// launch costs what they give.  One piece | slices, us: forward, 8 experts 1024 x 512
+// 6.7 | 9.0 in 2, x 1024 9.1 | 9.6 in 3, x 2048 14.2 | 11.6 in 3; row gradient, 2
+// experts 1024 x 512 14.8 | 12.6 in 4; 4 by 4 bits, 8 experts 1024 x 2048 8.7 | 10.7
+// in 2, x 4096 13.2 | 12.2 in 3, x 8192 29.3 | 17.7 in 3.  Odd sizes: 8 experts 1024
+// x 1023 25.5 | 15.2 in 3.
 int product_slices(int mode, int R, int E, int N, int K) {
   if (R < 1) return 1;
   TileArgs a{};
@@ -859,31 +875,38 @@ int product_slices(int mode, int R, int E, int N, int K) {
   a.N = N;
   a.K = K;
   const int rows = R / E;
+  const bool odd = mode != FOUR && (K % 8 || (mode != FWD && N % 8));   // 128 x 128, two workgroups on a CU
   int64_t tiles, z, out, most = 1 << 22;   // values of all parts: 16 MB take no longer than a launch
-  int least = 256;                         // z of a slice
+  int least = 256, from = 1024;
   if (mode == FWD) {
-    tiles = rows <= FEW_ROWS ? workgroups<FWD>(a, 64, 128) : workgroups<FWD>(a, 128, 256);
+    tiles = odd ? workgroups<FWD>(a, 128, 128) : rows <= FEW_ROWS ? workgroups<FWD>(a, 64, 128) : workgroups<FWD>(a, 128, 256);
     z = K;
     out = (int64_t)R * N;
   } else if (mode == ROWS) {
-    tiles = workgroups<ROWS>(a, 128, 256);
+    tiles = odd ? workgroups<ROWS>(a, 128, 128) : workgroups<ROWS>(a, 128, 256);
     z = N;
     out = (int64_t)R * K;
   } else if (mode == WEIGHTS) {
     // one expert may have most of the rows: slices as if it were four times the
-    // mean, up to four times the CUs, and parts of up to 1 KB for each row (46000
+    // mean, up to four times the workgroups, and parts of up to 1 KB for each row (46000
     // rows unevenly to 26 experts, 1446 x 62: 1465 us in one piece, 133 in 4)
-    tiles = ((int64_t)E * ((N + 255) / 256) * ((K + 255) / 256) + 3) / 4;
+    const int64_t edge = odd ? 128 : 256;
+    tiles = (E * ((N + edge - 1) / edge) * ((K + edge - 1) / edge) + 3) / 4;
     z = std::min<int64_t>(R, (int64_t)rows * 4);
     most = std::max<int64_t>(most, (int64_t)R << 8);
+    from = 2048;
     out = (int64_t)E * N * K;
   } else {
     tiles = rows <= 32 ? workgroups<FOUR>(a, 64, 128) : workgroups<FOUR>(a, 128, 128);
     z = K;
     out = (int64_t)R * N;
     least = 1024;
+    from = 4096;
   }
-  const int64_t s = std::min({(int64_t)64, z / least, 256 / tiles, most / std::max<int64_t>(1, out)});   // 256 CUs
+  if (odd) from /= 2;
+  if (z < from) return 1;
+  const int64_t at_a_time = odd ? 512 : 256;
+  const int64_t s = std::min({(int64_t)64, z / least, at_a_time / tiles, most / std::max<int64_t>(1, out)});
   return (int)std::max<int64_t>(1, s);
 }
 
