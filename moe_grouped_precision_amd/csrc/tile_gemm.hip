@@ -51,7 +51,8 @@ typedef short v4s __attribute__((ext_vector_type(4)));
 typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 
 enum { FWD = PRODUCT_FWD, ROWS = PRODUCT_ROWS, WEIGHTS = PRODUCT_WEIGHTS, FOUR = PRODUCT_FOUR };
-constexpr int FEW_ROWS = 48, MANY_ROWS = 768;   // of an expert in the mean: see launch_bf16
+constexpr int FEW_ROWS = 48, MANY_ROWS = 768;   // of an expert in the mean: see tile_of
+constexpr int64_t CUS = 256;
 
 // What a chunk past the end of z is read from: zeros, so that whatever the
 // buffer holds there (another expert's rows, infinities) stays out of the sums.
@@ -263,30 +264,21 @@ struct Operands {
   }
 };
 
-// Four of the lane's results to out[y][x .. x+3].
-template <int MODE, typename OUT>
-__device__ __forceinline__ void put(const TileArgs& a, const Place& p, const Operands<MODE>& op, int y, int x, v4f v) {
+// Four of the lane's results added to a bf16 out[y][x .. x+3], with one rounding.
+template <int MODE>
+__device__ __forceinline__ void add_to(const TileArgs& a, const Place& p, const Operands<MODE>& op, int y, int x, v4f v) {
   if (y >= p.ny || x >= p.nx) return;
-  OUT* o = static_cast<OUT*>(a.out) + op.out0 +
-           (MODE == WEIGHTS ? (size_t)p.e * a.N + p.y0 + y : (size_t)(p.r0 + p.y0 + y)) * op.width + p.x0 + x;
-  const int n = a.wide ? 4 : min(4, p.nx - x);
-  if (MODE == WEIGHTS && a.accumulate) {
+  uint16_t* o = static_cast<uint16_t*>(a.out) + ((size_t)p.e * a.N + p.y0 + y) * op.width + p.x0 + x;
+  const int n = min(4, p.nx - x);
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    if (c < n) v[c] += __uint_as_float((uint32_t)o[c] << 16);
+  if (a.wide) {
+    store_bf16x4(o, v);
+  } else {
 #pragma unroll
     for (int c = 0; c < 4; ++c)
-      if (c < n) v[c] += sizeof(OUT) == 4 ? (float)o[c] : __uint_as_float((uint32_t)(uint16_t)o[c] << 16);
-  }
-  if constexpr (sizeof(OUT) == 4) {
-    if (a.wide) *reinterpret_cast<v4f*>(o) = v;
-    else
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (c < n) o[c] = v[c];
-  } else {
-    if (a.wide) store_bf16x4(o, v);
-    else
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (c < n) o[c] = __builtin_bit_cast(uint16_t, (__bf16)v[c]);
+      if (c < n) o[c] = __builtin_bit_cast(uint16_t, (__bf16)v[c]);
   }
 }
 
@@ -312,9 +304,9 @@ template <int MODE, int MX, typename OUT>
 __device__ __forceinline__ void put_block(const TileArgs& a, const Place& p, const Operands<MODE>& op, int y, int x,
                                           const v4f (&acc)[MX]) {
   const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
-  if (a.wide < 2 || (sizeof(OUT) == 2 && MODE == WEIGHTS && a.accumulate)) {
+  if (sizeof(OUT) == 2 && MODE == WEIGHTS && a.accumulate) {
 #pragma unroll
-    for (int j = 0; j < MX; ++j) put<MODE, OUT>(a, p, op, y + i, x + 16 * j + 4 * q, acc[j]);
+    for (int j = 0; j < MX; ++j) add_to<MODE>(a, p, op, y + i, x + 16 * j + 4 * q, acc[j]);
     return;
   }
   constexpr int PER = 16 / sizeof(OUT), PAIRS = MX * 16 / (4 * PER) / 2;   // values of a store, pairs of stores
@@ -322,10 +314,29 @@ __device__ __forceinline__ void put_block(const TileArgs& a, const Place& p, con
     if (row >= p.ny || col >= p.nx) return;
     OUT* o = static_cast<OUT*>(a.out) + op.out0 +
              (MODE == WEIGHTS ? (size_t)p.e * a.N + p.y0 + row : (size_t)(p.r0 + p.y0 + row)) * op.width + p.x0 + col;
-    v4i* const at = reinterpret_cast<v4i*>(o);
-    if (sizeof(OUT) == 4 && MODE == WEIGHTS && a.accumulate)
-      v = __builtin_bit_cast(v4i, __builtin_bit_cast(v4f, v) + *reinterpret_cast<const v4f*>(o));
-    __builtin_nontemporal_store(v, at);
+    if (a.wide) {
+      if (sizeof(OUT) == 4 && MODE == WEIGHTS && a.accumulate)
+        v = __builtin_bit_cast(v4i, __builtin_bit_cast(v4f, v) + *reinterpret_cast<const v4f*>(o));
+      __builtin_nontemporal_store(v, reinterpret_cast<v4i*>(o));
+      return;
+    }
+    // rows at any address: 16 bytes all the same, a row's end value by value
+    const int n = min(PER, p.nx - col);
+    if (sizeof(OUT) == 4 && MODE == WEIGHTS && a.accumulate) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (c < n) v[c] = __float_as_int(__int_as_float(v[c]) + (float)o[c]);
+    }
+    if (n == PER) {
+      __builtin_memcpy(o, &v, 16);
+    } else {
+#pragma unroll
+      for (int c = 0; c < PER - 1; ++c)
+        if (c < n) {
+          if constexpr (sizeof(OUT) == 4) o[c] = __int_as_float(v[c]);
+          else o[c] = (uint16_t)((uint32_t)v[c >> 1] >> (16 * (c & 1)));
+        }
+    }
   };
   v4i v[MX * 16 / (4 * PER)];
   if constexpr (sizeof(OUT) == 4) {
@@ -469,9 +480,7 @@ struct General {
     if (MODE == WEIGHTS && a.accumulate && steps == 0) return;
 #pragma unroll
     for (int i = 0; i < M; ++i)
-#pragma unroll
-      for (int j = 0; j < M; ++j)
-        put<MODE, OUT>(a, p, op, (wy * M + i) * 16 + (lane & 15), (wx * M + j) * 16 + 4 * (lane >> 4), acc[i][j]);
+      put_block<MODE, M, OUT>(a, p, op, (wy * M + i) * 16, wx * M * 16, acc[i]);
   }
 };
 
@@ -780,10 +789,7 @@ join_kernel(TileArgs a, const float* __restrict__ parts) {
 bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 template <typename OUT>
-int wide_out(const TileArgs& a, int width) {
-  if (width % (16 / sizeof(OUT)) == 0 && aligned_to(a.out, 16)) return 2;
-  return width % 4 == 0 && aligned_to(a.out, 4 * sizeof(OUT));
-}
+bool wide_out(const TileArgs& a, int width) { return width % (16 / sizeof(OUT)) == 0 && aligned_to(a.out, 16); }
 
 // Where a product has fewer tiles than the chip has CUs and a long sum, the sum is
 // cut into slices (parts of fp32 in the workspace, added in order): 3 rows, 128 x
@@ -833,28 +839,45 @@ hipError_t launch_odd(const TileArgs& a, hipStream_t stream) {
 // the weights only with 256 columns (127 against 103).  The weights' gradient has
 // its largest tiles at any number of rows (16: 671 against 750 us with 128 x 256,
 // 288: 1133 / 1253, 1024: 2070 / 2282).
+// A tile also needs enough of its kind: if there are half as many as CUs or fewer, the
+// next smaller ones are done in one round as well, in less time (8 experts, 8192 rows,
+// 512 x 4096: forward 80 us with the largest, 47; 4 by 4 bits 34, 20; 7384 rows, 256 x
+// 2864, forward 49, 24; but 24000 rows, 512 x 2048: 48, 58 with 1.5 rounds).
+enum { SMALL, MIDDLE, LARGE };
+template <int MODE>
+int tile_of(const TileArgs& a) {
+  const int rows = a.R / a.E;
+  if (MODE == FOUR) {
+    // as above; 16 rows: 84, 88 and 108 us with these three, 64: 134, 125 and 125,
+    // 128: 186, 159 and 170, 288: 311, 243 and 239, 1024: 882, 671 and 576
+    if (rows <= 32) return SMALL;
+    return rows <= 200 || workgroups<MODE>(a, 256, 256) <= CUS / 2 ? MIDDLE : LARGE;
+  }
+  if (MODE == WEIGHTS) return LARGE;
+  if (MODE == FWD && (rows <= FEW_ROWS || workgroups<MODE>(a, 128, 256) <= CUS / 2)) return SMALL;
+  return rows <= MANY_ROWS || workgroups<MODE>(a, 256, 256) <= CUS / 2 ? MIDDLE : LARGE;
+}
+
 template <int MODE, typename OUT>
 hipError_t launch_bf16(const TileArgs& a, hipStream_t stream) {
-  const int rows = a.R / a.E;
   // Whole chunks: along K of the forward product's rows, along both of the others.
   // A tile's offsets within an operand are 32 bits: 256 rows, or 64 of z, of 8 MB
   // at most.
   if (a.K % 8 || (MODE != FWD && a.N % 8) || !aligned_to(a.Y, 16) || !aligned_to(a.X, 16) || a.N > (1 << 22))
     return launch_odd<MODE, OUT>(a, stream);
+  const int tile = tile_of<MODE>(a);
   if constexpr (MODE == FWD)
-    if (rows <= FEW_ROWS) return launch<MODE, Direct<MODE, 64, 128, 1, 4, 3, OUT>>(a, stream);
+    if (tile == SMALL) return launch<MODE, Direct<MODE, 64, 128, 1, 4, 3, OUT>>(a, stream);
   if constexpr (MODE != WEIGHTS)
-    if (rows <= MANY_ROWS) return launch<MODE, Direct<MODE, 128, 256, 2, 4, 3, OUT>>(a, stream);
+    if (tile == MIDDLE) return launch<MODE, Direct<MODE, 128, 256, 2, 4, 3, OUT>>(a, stream);
   return launch<MODE, Direct<MODE, 256, 256, 2, 4, 2, OUT>>(a, stream);
 }
 
 template <typename OUT>
 hipError_t launch_four(const TileArgs& a, hipStream_t stream) {
-  // as above; 16 rows: 84, 88 and 108 us with these three, 64: 134, 125 and 125,
-  // 128: 186, 159 and 170, 288: 311, 243 and 239, 1024: 882, 671 and 576
-  const int rows = a.R / a.E;
-  if (rows <= 32) return launch<FOUR, Direct<FOUR, 64, 128, 1, 4, 2, OUT>>(a, stream);
-  if (rows <= 200) return launch<FOUR, Direct<FOUR, 128, 128, 2, 2, 2, OUT>>(a, stream);
+  const int tile = tile_of<FOUR>(a);
+  if (tile == SMALL) return launch<FOUR, Direct<FOUR, 64, 128, 1, 4, 2, OUT>>(a, stream);
+  if (tile == MIDDLE) return launch<FOUR, Direct<FOUR, 128, 128, 2, 2, 2, OUT>>(a, stream);
   return launch<FOUR, Direct<FOUR, 256, 256, 2, 4, 2, OUT>>(a, stream);
 }
 
@@ -879,7 +902,7 @@ int product_slices(int mode, int R, int E, int N, int K) {
   int64_t tiles, z, out, most = 1 << 22;   // values of all parts: 16 MB take no longer than a launch
   int least = 256, from = 1024;
   if (mode == FWD) {
-    tiles = odd ? workgroups<FWD>(a, 128, 128) : rows <= FEW_ROWS ? workgroups<FWD>(a, 64, 128) : workgroups<FWD>(a, 128, 256);
+    tiles = odd ? workgroups<FWD>(a, 128, 128) : tile_of<FWD>(a) == SMALL ? workgroups<FWD>(a, 64, 128) : CUS;
     z = K;
     out = (int64_t)R * N;
   } else if (mode == ROWS) {
@@ -897,7 +920,7 @@ int product_slices(int mode, int R, int E, int N, int K) {
     from = 2048;
     out = (int64_t)E * N * K;
   } else {
-    tiles = rows <= 32 ? workgroups<FOUR>(a, 64, 128) : workgroups<FOUR>(a, 128, 128);
+    tiles = tile_of<FOUR>(a) == SMALL ? workgroups<FOUR>(a, 64, 128) : workgroups<FOUR>(a, 128, 128);
     z = K;
     out = (int64_t)R * N;
     least = 1024;
@@ -905,7 +928,7 @@ int product_slices(int mode, int R, int E, int N, int K) {
   }
   if (odd) from /= 2;
   if (z < from) return 1;
-  const int64_t at_a_time = odd ? 512 : 256;
+  const int64_t at_a_time = odd ? 2 * CUS : CUS;
   const int64_t s = std::min({(int64_t)64, z / least, at_a_time / tiles, most / std::max<int64_t>(1, out)});
   return (int)std::max<int64_t>(1, s);
 }

@@ -150,7 +150,7 @@ struct TileArgs {
   const int32_t* offsets;  // [E+1]
   void* out;
   int E, R, N, K, accumulate;
-  int slices, wide;        // of z; outputs 0 one by one, 1 in whole 4s, 2 in 16 bytes (both set at the launch)
+  int slices, wide;        // of z; outputs in whole 16 bytes (both set at the launch)
 };
 enum { PRODUCT_FWD = 0, PRODUCT_ROWS = 1, PRODUCT_WEIGHTS = 2, PRODUCT_FOUR = 3 };
 // Slices of a product's sum, and the bytes of their parts (0 for one slice).
