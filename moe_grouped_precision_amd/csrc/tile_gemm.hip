@@ -34,6 +34,7 @@
 //
 // X is the matrix instruction's first operand, so a lane's four results are four
 // consecutive x of one y.
+#include "tile_place.h"
 #include "w4a8_kernel.h"
 #include "w4a8_launch.h"
 
@@ -136,7 +137,7 @@ __device__ __forceinline__ bool find_tile(const TileArgs& a, int64_t b, Place& p
   for (int i = lane; i < a.E; i += 64) {
     const int o0 = a.offsets[i], o1 = a.offsets[i + 1];
     bad |= o1 < o0 || (i == 0 && o0 != 0) || (i == a.E - 1 && o1 > a.R);
-    if (MODE != WEIGHTS) sum += (int)((uint32_t)(o1 - o0 + TY - 1) / TY);
+    if (MODE != WEIGHTS) sum += pieces_of(o1 - o0, TY);   // of no use where bad
   }
   if (__ballot(bad)) return false;
   int64_t t;
@@ -158,7 +159,7 @@ __device__ __forceinline__ bool find_tile(const TileArgs& a, int64_t b, Place& p
     int before = 0;
     for (int base = 0;; base += 64) {
       const int i = base + lane;
-      const int n = i < a.E ? (a.offsets[i + 1] - a.offsets[i] + TY - 1) / TY : 0;
+      const int n = i < a.E ? pieces_of(a.offsets[i + 1] - a.offsets[i], TY) : 0;
       const int upto = before + wave_inclusive_sum(n);
       const uint64_t hit = __ballot(m < upto);   // m < total: some lane has it
       if (hit) {
@@ -183,7 +184,7 @@ __device__ __forceinline__ bool find_tile(const TileArgs& a, int64_t b, Place& p
   } else {
     // an expert's rows in equal tiles of whole blocks of 16: the kernel leaves
     // out blocks that a tile does not have
-    const int per = ((p.rows + mine - 1) / mine + 15) & ~15;
+    const int per = rows_per_tile(p.rows, mine);
     p.y0 = uniform(yt * per);
     p.ny = uniform(min(per, p.rows - p.y0));
   }
@@ -251,16 +252,12 @@ struct Operands {
                         : a.X + ((size_t)p.e * a.N + p.x0) * xbytes;
     out0 = 0;
     if (a.slices > 1) {
-      const int z0 = min(zn, (int)blockIdx.y * slice_of(zn, a.slices));
-      zn = min(zn - z0, slice_of(zn, a.slices));
+      const int each = slice_of(zn, a.slices, MODE == FOUR ? 512 : 64), z0 = min(zn, (int)blockIdx.y * each);
+      zn = min(zn - z0, each);
       Y += YT ? (size_t)z0 * ybytes : MODE == FOUR ? z0 / 2 : z0 * 2;
       X += XT ? (size_t)z0 * xbytes : MODE == FOUR ? z0 / 2 : z0 * 2;
       out0 = (size_t)blockIdx.y * (MODE == WEIGHTS ? (size_t)a.E * a.N : (size_t)a.R) * width;
     }
-  }
-  static __device__ __forceinline__ int slice_of(int z, int slices) {
-    constexpr int STEP = MODE == FOUR ? 512 : 64;
-    return (z / slices + STEP) / STEP * STEP;   // slices * this > z
   }
 };
 
@@ -391,7 +388,7 @@ struct General {
     if (!find_tile<MODE, TY, TX>(a, b, p)) return;
     const Operands<MODE> op(a, p);
     constexpr bool YT = Operands<MODE>::YT, XT = Operands<MODE>::XT;
-    const int steps = (op.zn + ZSTEP - 1) / ZSTEP;
+    const int steps = pieces_of(op.zn, ZSTEP);
     v4f acc[M][M];
 #pragma unroll
     for (int i = 0; i < M; ++i)
@@ -517,7 +514,7 @@ struct Direct {
     if (!find_tile<MODE, TY, TX>(a, b, p)) return;
     const Operands<MODE> op(a, p);
     constexpr bool YT = Operands<MODE>::YT, XT = Operands<MODE>::XT;
-    const int steps = (op.zn + ZSTEP - 1) / ZSTEP;
+    const int steps = pieces_of(op.zn, ZSTEP);
     const int full = op.zn / ZSTEP;   // steps without an end of z in them
     v4f acc[MY][MX];
 #pragma unroll
@@ -554,7 +551,7 @@ struct Direct {
         if (i < IY) chunk_of<TY, YT, KS>(j, lane, row, chunk);
         else chunk_of<TX, XT, KS>(j, lane, row, chunk);
         const int z = (i < IY ? YT : XT) ? row : chunk * (MODE == FOUR ? 32 : 8);
-        dma16(s * ZSTEP + z < op.zn ? base + off[i] : reinterpret_cast<const uint8_t*>(&zero_chunk), place(i, stage));
+        dma16(inside(s, ZSTEP, z, op.zn) ? base + off[i] : reinterpret_cast<const uint8_t*>(&zero_chunk), place(i, stage));
       }
     };
     // Every second tile takes the whole steps of a pair the other way round, so that
@@ -642,7 +639,7 @@ struct Direct {
     uint32_t stage = 0, spare = (NS - 1) * STAGE;
     auto step = [&](int s, auto whole_, auto all_) {
       constexpr bool WHOLE = decltype(whole_)::value, ALL = decltype(all_)::value;
-      const bool two = WHOLE || s * ZSTEP + ZSTEP / 2 < op.zn;   // the second half has z
+      const bool two = WHOLE || inside(s, ZSTEP, ZSTEP / 2, op.zn);   // the second half has z
       const bool more = WHOLE || s + NS - 1 < steps, last = !WHOLE && s + 1 >= steps;
       const uint32_t after = stage == (NS - 1) * STAGE ? 0 : stage + STAGE;
       if (MODE == FOUR && !(s & 1)) scales(s);
