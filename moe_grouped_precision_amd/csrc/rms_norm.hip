@@ -479,7 +479,7 @@ hipError_t launch_rms_norm(const NormArgs& a, hipStream_t stream) {
   while ((chunks + nch - 1) / nch > most) nch *= 2;
   const int threads = ((chunks + nch - 1) / nch + 63) / 64 * 64;
   const int rows_per = threads == 64 ? 4 : 1, block = threads * rows_per;
-  return in_launches((a.T + rows_per - 1) / rows_per, block, [&](int64_t b, int64_t n) {
+  return in_launches(((int64_t)a.T + rows_per - 1) / rows_per, block, [&](int64_t b, int64_t n) {
     const dim3 grid((unsigned)n), blk(block);
     const int64_t t = b * rows_per;
 #define W4A8_NORM(N)                                                                              \
