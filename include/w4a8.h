@@ -735,7 +735,7 @@ int w4a8_grouped_gemm_a4(const uint8_t* A_fp4_dev, const uint8_t* a_scales_dev, 
 /*
  * w4a8_clip_grads -- the norm of n tensors as one vector and their scaling by it:
  *   norm = sqrt(sum over all tensors of x^2),  c = min(1, max_norm / (norm + eps)),
- *   out = c * x   (the product in fp32, rounded to the tensor's type)
+ *   out = c * x   (c to 24 bits at any size, the product in fp32, rounded to the tensor's type)
  * Squares and sums are in 64 bits.  A NaN or infinite gradient makes the norm
  * NaN or infinite, and the outputs what the formula gives (NaN; 0 or NaN).
  *

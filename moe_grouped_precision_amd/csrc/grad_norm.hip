@@ -134,6 +134,18 @@ norm_kernel(double* partials, int parts, float* __restrict__ norm) {
   }
 }
 
+// min(1, ratio) as c * d.  d is 1 where fp32 holds c whole; below, where norms are
+// 2^126 times max_norm and more (fp32 alone left c fewer bits there, and 0 below
+// 2^-150), d is a power of two that keeps c at 2^-100 or, past d's own range, as
+// near as it gets: x c then is an ordinary number wherever x c d is not zero.
+struct Factor { float c, d; };
+__device__ __forceinline__ Factor factor_of(double ratio) {
+  if (ratio > 1.0) return {1.0f, 1.0f};
+  if (!(ratio > 0.0 && ratio < 0x1p-126)) return {(float)ratio, 1.0f};   // NaN and 0 among them
+  const int e = max(__builtin_amdgcn_frexp_exp(ratio) + 100, -149);
+  return {(float)ldexp(ratio, -e), ldexpf(1.0f, e)};
+}
+
 // c is 1 exactly, and x its own result, for all norms up to max_norm; a NaN
 // norm makes c, and so every gradient, NaN.  in may be out.  Everything passes
 // here once: past the caches (2.1 GB of norm, read and write 516 us, 564 through
@@ -147,7 +159,8 @@ clip_kernel(const Tensors t, const double* partials, int parts, float max_norm, 
   const double nv = sqrt(sum_of(partials, parts, s));
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)nv;
   const double ratio = (double)max_norm / (nv + (double)eps);
-  const float c = ratio > 1.0 ? 1.0f : (float)ratio;
+  const Factor f = factor_of(ratio);
+  const float c = f.c, d = f.d;
   for (uint32_t ch = blockIdx.x; ch < t.chunks; ch += gridDim.x) {
     const int i = tensor_of(t, ch);
     if (c == 1.0f && t.in[i] == t.out[i]) continue;   // nothing to change
@@ -163,11 +176,11 @@ clip_kernel(const Tensors t, const double* partials, int parts, float max_norm, 
         for (int e = threadIdx.x * 4; e < done; e += GN_THREADS * 4) {
           v4u v = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(p + e));
 #pragma unroll
-          for (int j = 0; j < 4; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * c);
+          for (int j = 0; j < 4; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * c * d);
           __builtin_nontemporal_store(v, reinterpret_cast<v4u*>(o + e));
         }
       }
-      for (int e = done + threadIdx.x; e < n; e += GN_THREADS) o[e] = p[e] * c;
+      for (int e = done + threadIdx.x; e < n; e += GN_THREADS) o[e] = p[e] * c * d;
     } else {
       const uint16_t* p = static_cast<const uint16_t*>(t.in[i]) + at;
       uint16_t* o = static_cast<uint16_t*>(t.out[i]) + at;
@@ -178,14 +191,14 @@ clip_kernel(const Tensors t, const double* partials, int parts, float max_norm, 
           v4u v = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(p + e));
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const v2f x = {__uint_as_float(v[j] << 16) * c, __uint_as_float(v[j] & 0xffff0000u) * c};
+            const v2f x = {__uint_as_float(v[j] << 16) * c * d, __uint_as_float(v[j] & 0xffff0000u) * c * d};
             v[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector(x, v2bf));
           }
           __builtin_nontemporal_store(v, reinterpret_cast<v4u*>(o + e));
         }
       }
       for (int e = done + threadIdx.x; e < n; e += GN_THREADS)
-        o[e] = __builtin_bit_cast(uint16_t, (__bf16)(__uint_as_float((uint32_t)p[e] << 16) * c));
+        o[e] = __builtin_bit_cast(uint16_t, (__bf16)(__uint_as_float((uint32_t)p[e] << 16) * c * d));
     }
   }
 }
