@@ -648,6 +648,9 @@ size_t w4a8_rms_norm_backward_bytes(int T, int K);
  */
 enum { W4A8_PRODUCT_BF16 = 0, W4A8_PRODUCT_DGRAD = 1, W4A8_PRODUCT_WGRAD = 2, W4A8_PRODUCT_A4 = 3 };
 size_t w4a8_grouped_gemm_workspace_bytes(int product, int R, int E, int N, int K);
+/* The tile of a product's kernel, rows << 16 | columns of its output, with operands at 16-byte alignment; 0 for
+   sizes it refuses and for R == 0.  For information, like w4a8_plan_params. */
+int w4a8_grouped_gemm_tile(int product, int R, int E, int N, int K);
 int w4a8_grouped_gemm_bf16(const uint16_t* A_bf16_dev, const uint16_t* W_bf16_dev, const int32_t* expert_offsets_dev,
                            int R, int E, int N, int K, uint16_t* C_bf16_dev, void* workspace_dev, size_t workspace_bytes,
                            void* stream);

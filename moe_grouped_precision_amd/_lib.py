@@ -99,6 +99,8 @@ def _declare(lib):
     lib.w4a8_quantize_gather_fp4.restype = i32
     lib.w4a8_grouped_gemm_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
     lib.w4a8_grouped_gemm_workspace_bytes.restype = sz
+    lib.w4a8_grouped_gemm_tile.argtypes = [i32, i32, i32, i32, i32]
+    lib.w4a8_grouped_gemm_tile.restype = i32
     lib.w4a8_grouped_gemm_a4.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, sz, vp]
     lib.w4a8_grouped_gemm_a4.restype = i32
     lib.w4a8_clip_grads.argtypes = [vp, vp, vp, vp, i32, f32, f32, vp, sz, vp, vp]

@@ -724,6 +724,13 @@ size_t w4a8_grouped_gemm_workspace_bytes(int product, int R, int E, int N, int K
   return w4a8::product_workspace(product, R, E, N, K);
 }
 
+int w4a8_grouped_gemm_tile(int product, int R, int E, int N, int K) {
+  if (product < W4A8_PRODUCT_BF16 || product > W4A8_PRODUCT_A4 || R < 1 || E < 1 || E > W4A8_MAX_EXPERTS || N < 1 ||
+      N > W4A8_MAX_N || K < 1 || K > W4A8_MAX_K || (product == W4A8_PRODUCT_A4 && (N % 32 || K % 128)))
+    return 0;
+  return w4a8::product_tile(product, R, E, N, K);
+}
+
 int w4a8_grouped_gemm_bf16(const uint16_t* A_bf16_dev, const uint16_t* W_bf16_dev, const int32_t* expert_offsets_dev,
                            int R, int E, int N, int K, uint16_t* C_bf16_dev, void* workspace_dev, size_t workspace_bytes,
                            void* stream) {

@@ -840,7 +840,15 @@ hipError_t launch_odd(const TileArgs& a, hipStream_t stream) {
 // next smaller ones are done in one round as well, in less time (8 experts, 8192 rows,
 // 512 x 4096: forward 80 us with the largest, 47; 4 by 4 bits 34, 20; 7384 rows, 256 x
 // 2864, forward 49, 24; but 24000 rows, 512 x 2048: 48, 58 with 1.5 rounds).
-enum { SMALL, MIDDLE, LARGE };
+enum { SMALL, MIDDLE, LARGE, ODD };
+struct TileSize { int y, x; };
+constexpr TileSize size_of(int mode, int tile) {
+  return tile == SMALL ? TileSize{64, 128} : tile == LARGE ? TileSize{256, 256}
+         : tile == MIDDLE && mode != FOUR ? TileSize{128, 256} : TileSize{128, 128};
+}
+template <int MODE, int TILE, typename OUT>
+using DirectTile = Direct<MODE, size_of(MODE, TILE).y, size_of(MODE, TILE).x, TILE == SMALL ? 1 : 2,
+                          MODE == FOUR && TILE == MIDDLE ? 2 : 4, MODE == FOUR || TILE == LARGE ? 2 : 3, OUT>;
 template <int MODE>
 int tile_of(const TileArgs& a) {
   const int rows = a.R / a.E;
@@ -855,27 +863,31 @@ int tile_of(const TileArgs& a) {
   return rows <= MANY_ROWS || workgroups<MODE>(a, 256, 256) <= CUS / 2 ? MIDDLE : LARGE;
 }
 
+// Whole chunks: along K of the forward product's rows, along both of the others.
+// A tile's offsets within an operand are 32 bits: 256 rows, or 64 of z, of 8 MB
+// at most.
+bool odd_sizes(int mode, int N, int K) {
+  return mode != FOUR && (K % 8 || (mode != FWD && N % 8) || N > (1 << 22));
+}
+
 template <int MODE, typename OUT>
 hipError_t launch_bf16(const TileArgs& a, hipStream_t stream) {
-  // Whole chunks: along K of the forward product's rows, along both of the others.
-  // A tile's offsets within an operand are 32 bits: 256 rows, or 64 of z, of 8 MB
-  // at most.
-  if (a.K % 8 || (MODE != FWD && a.N % 8) || !aligned_to(a.Y, 16) || !aligned_to(a.X, 16) || a.N > (1 << 22))
+  if (odd_sizes(MODE, a.N, a.K) || !aligned_to(a.Y, 16) || !aligned_to(a.X, 16))
     return launch_odd<MODE, OUT>(a, stream);
   const int tile = tile_of<MODE>(a);
   if constexpr (MODE == FWD)
-    if (tile == SMALL) return launch<MODE, Direct<MODE, 64, 128, 1, 4, 3, OUT>>(a, stream);
+    if (tile == SMALL) return launch<MODE, DirectTile<MODE, SMALL, OUT>>(a, stream);
   if constexpr (MODE != WEIGHTS)
-    if (tile == MIDDLE) return launch<MODE, Direct<MODE, 128, 256, 2, 4, 3, OUT>>(a, stream);
-  return launch<MODE, Direct<MODE, 256, 256, 2, 4, 2, OUT>>(a, stream);
+    if (tile == MIDDLE) return launch<MODE, DirectTile<MODE, MIDDLE, OUT>>(a, stream);
+  return launch<MODE, DirectTile<MODE, LARGE, OUT>>(a, stream);
 }
 
 template <typename OUT>
 hipError_t launch_four(const TileArgs& a, hipStream_t stream) {
   const int tile = tile_of<FOUR>(a);
-  if (tile == SMALL) return launch<FOUR, Direct<FOUR, 64, 128, 1, 4, 2, OUT>>(a, stream);
-  if (tile == MIDDLE) return launch<FOUR, Direct<FOUR, 128, 128, 2, 2, 2, OUT>>(a, stream);
-  return launch<FOUR, Direct<FOUR, 256, 256, 2, 4, 2, OUT>>(a, stream);
+  if (tile == SMALL) return launch<FOUR, DirectTile<FOUR, SMALL, OUT>>(a, stream);
+  if (tile == MIDDLE) return launch<FOUR, DirectTile<FOUR, MIDDLE, OUT>>(a, stream);
+  return launch<FOUR, DirectTile<FOUR, LARGE, OUT>>(a, stream);
 }
 
 }  // namespace
@@ -928,6 +940,20 @@ int product_slices(int mode, int R, int E, int N, int K) {
   const int64_t at_a_time = odd ? 2 * CUS : CUS;
   const int64_t s = std::min({(int64_t)64, z / least, at_a_time / tiles, most / std::max<int64_t>(1, out)});
   return (int)std::max<int64_t>(1, s);
+}
+
+int product_tile(int mode, int R, int E, int N, int K) {
+  TileArgs a{};
+  a.R = R;
+  a.E = E;
+  a.N = N;
+  a.K = K;
+  const int tile = odd_sizes(mode, N, K) ? ODD
+                   : mode == FWD     ? tile_of<FWD>(a)
+                   : mode == ROWS    ? tile_of<ROWS>(a)
+                   : mode == WEIGHTS ? tile_of<WEIGHTS>(a)
+                                     : tile_of<FOUR>(a);
+  return size_of(mode, tile).y << 16 | size_of(mode, tile).x;
 }
 
 size_t product_workspace(int mode, int R, int E, int N, int K) {

@@ -156,6 +156,8 @@ enum { PRODUCT_FWD = 0, PRODUCT_ROWS = 1, PRODUCT_WEIGHTS = 2, PRODUCT_FOUR = 3 
 // Slices of a product's sum, and the bytes of their parts (0 for one slice).
 int product_slices(int product, int R, int E, int N, int K);
 size_t product_workspace(int product, int R, int E, int N, int K);
+// Its tile, rows << 16 | columns, for operands at 16-byte alignment.
+int product_tile(int product, int R, int E, int N, int K);
 // work: product_workspace() bytes, or null for one slice in any case
 hipError_t launch_grouped_bf16(const TileArgs& args, void* work, hipStream_t stream);
 hipError_t launch_grouped_dgrad(const TileArgs& args, void* work, hipStream_t stream);
