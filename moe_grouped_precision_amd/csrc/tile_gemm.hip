@@ -849,6 +849,16 @@ constexpr TileSize size_of(int mode, int tile) {
 template <int MODE, int TILE, typename OUT>
 using DirectTile = Direct<MODE, size_of(MODE, TILE).y, size_of(MODE, TILE).x, TILE == SMALL ? 1 : 2,
                           MODE == FOUR && TILE == MIDDLE ? 2 : 4, MODE == FOUR || TILE == LARGE ? 2 : 3, OUT>;
+// Tiles whose sums product_slices() may cut: the others come in numbers that fill
+// the chip, and their kernels for parts in fp32 do not exist.
+constexpr bool in_slices(int mode, int tile) {
+  return tile == ODD || mode == WEIGHTS || tile == (mode == ROWS ? MIDDLE : SMALL) || (mode == FOUR && tile == MIDDLE);
+}
+template <int MODE, int TILE, typename OUT>
+hipError_t launch_tile(const TileArgs& a, hipStream_t stream) {
+  if constexpr (sizeof(OUT) == 4 && !in_slices(MODE, TILE)) return hipErrorInvalidValue;
+  else return launch<MODE, DirectTile<MODE, TILE, OUT>>(a, stream);
+}
 template <int MODE>
 int tile_of(const TileArgs& a) {
   const int rows = a.R / a.E;
@@ -861,6 +871,11 @@ int tile_of(const TileArgs& a) {
   if (MODE == WEIGHTS) return LARGE;
   if (MODE == FWD && (rows <= FEW_ROWS || workgroups<MODE>(a, 128, 256) <= CUS / 2)) return SMALL;
   return rows <= MANY_ROWS || workgroups<MODE>(a, 256, 256) <= CUS / 2 ? MIDDLE : LARGE;
+}
+
+int tile_for(int mode, const TileArgs& a) {
+  return mode == FWD ? tile_of<FWD>(a) : mode == ROWS ? tile_of<ROWS>(a) : mode == WEIGHTS ? tile_of<WEIGHTS>(a)
+                                                                                           : tile_of<FOUR>(a);
 }
 
 // Whole chunks: along K of the forward product's rows, along both of the others.
@@ -876,18 +891,18 @@ hipError_t launch_bf16(const TileArgs& a, hipStream_t stream) {
     return launch_odd<MODE, OUT>(a, stream);
   const int tile = tile_of<MODE>(a);
   if constexpr (MODE == FWD)
-    if (tile == SMALL) return launch<MODE, DirectTile<MODE, SMALL, OUT>>(a, stream);
+    if (tile == SMALL) return launch_tile<MODE, SMALL, OUT>(a, stream);
   if constexpr (MODE != WEIGHTS)
-    if (tile == MIDDLE) return launch<MODE, DirectTile<MODE, MIDDLE, OUT>>(a, stream);
-  return launch<MODE, DirectTile<MODE, LARGE, OUT>>(a, stream);
+    if (tile == MIDDLE) return launch_tile<MODE, MIDDLE, OUT>(a, stream);
+  return launch_tile<MODE, LARGE, OUT>(a, stream);
 }
 
 template <typename OUT>
 hipError_t launch_four(const TileArgs& a, hipStream_t stream) {
   const int tile = tile_of<FOUR>(a);
-  if (tile == SMALL) return launch<FOUR, DirectTile<FOUR, SMALL, OUT>>(a, stream);
-  if (tile == MIDDLE) return launch<FOUR, DirectTile<FOUR, MIDDLE, OUT>>(a, stream);
-  return launch<FOUR, DirectTile<FOUR, LARGE, OUT>>(a, stream);
+  if (tile == SMALL) return launch_tile<FOUR, SMALL, OUT>(a, stream);
+  if (tile == MIDDLE) return launch_tile<FOUR, MIDDLE, OUT>(a, stream);
+  return launch_tile<FOUR, LARGE, OUT>(a, stream);
 }
 
 }  // namespace
@@ -908,10 +923,11 @@ int product_slices(int mode, int R, int E, int N, int K) {
   a.K = K;
   const int rows = R / E;
   const bool odd = mode != FOUR && (K % 8 || (mode != FWD && N % 8));   // 128 x 128, two workgroups on a CU
+  if (!odd && !in_slices(mode, tile_for(mode, a))) return 1;
   int64_t tiles, z, out, most = 1 << 22;   // values of all parts: 16 MB take no longer than a launch
   int least = 256, from = 1024;
   if (mode == FWD) {
-    tiles = odd ? workgroups<FWD>(a, 128, 128) : tile_of<FWD>(a) == SMALL ? workgroups<FWD>(a, 64, 128) : CUS;
+    tiles = odd ? workgroups<FWD>(a, 128, 128) : workgroups<FWD>(a, 64, 128);
     z = K;
     out = (int64_t)R * N;
   } else if (mode == ROWS) {
@@ -948,11 +964,7 @@ int product_tile(int mode, int R, int E, int N, int K) {
   a.E = E;
   a.N = N;
   a.K = K;
-  const int tile = odd_sizes(mode, N, K) ? ODD
-                   : mode == FWD     ? tile_of<FWD>(a)
-                   : mode == ROWS    ? tile_of<ROWS>(a)
-                   : mode == WEIGHTS ? tile_of<WEIGHTS>(a)
-                                     : tile_of<FOUR>(a);
+  const int tile = odd_sizes(mode, N, K) ? ODD : tile_for(mode, a);
   return size_of(mode, tile).y << 16 | size_of(mode, tile).x;
 }
 
