@@ -311,7 +311,8 @@ rms_norm_long_kernel(NormArgs a, int64_t row0) {
 }
 
 // The gradient: workgroup b takes rows b, b + gridDim.x, ... and keeps its part
-// of dw in registers, written to partials[b][K] at the end.
+// of dw in registers, an fp32 sum of ceil(T / 512) products (in 64 bits it would
+// take twice the registers), written to partials[b][K] at the end.
 template <int NCH, bool VEC>
 __global__ void __launch_bounds__(64 * GRAD_WAVES)
 rms_norm_backward_kernel(NormGradArgs a) {

@@ -1,7 +1,16 @@
-"""The norm of as many rows as its argument may name."""
+"""The norm of as many rows as its argument may name, and long sums of the weight
+gradient.
 
+The weight gradient's bound: a workgroup's part is an fp32 sum of ceil(T / 512)
+products, one rounding each (2^-24 of the magnitudes' sum), of an xh off by
+2^-21; the parts are added in 64 bits and rounded once: (ceil(T / 512) + 10)
+2^-24 of the magnitudes' sum."""
+
+import numpy as np
 import pytest
 import torch
+
+from oracle import bf16_rne_bits, norm
 
 pytestmark = pytest.mark.gpu
 
@@ -23,3 +32,14 @@ def test_as_many_rows_as_an_int_names(gpu_lib, T):
     assert all(float(f[r]) == (0.5 if r % 2 else -0.5) for r in spots)
     del x, y, f
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("T,K", [(16384, 64), (16383, 200), (5000, 33), (40000, 8)])
+def test_weight_gradient_over_many_rows(gpu_lib, T, K):
+    rng = np.random.default_rng(T + K)
+    h, dy = bf16_rne_bits(rng.standard_normal((T, K))), bf16_rne_bits(rng.standard_normal((T, K)))
+    dev = lambda b: torch.from_numpy(b.view(np.int16).copy()).view(torch.bfloat16).cuda()
+    _, dw, _, wmag = norm.rms_norm_backward_f64(h, None, dy, 1e-5)
+    _, got = gpu_lib.rms_norm_backward(dev(h), None, dev(dy), 1e-5)
+    bound = (-(-T // 512) + 10) * 2.0 ** -24 * wmag + 2.0 ** -149
+    assert np.max(np.abs(got.cpu().numpy() - dw) / bound) <= 1.0
