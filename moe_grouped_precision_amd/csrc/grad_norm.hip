@@ -146,8 +146,9 @@ __device__ __forceinline__ Factor factor_of(double ratio) {
   return {(float)ldexp(ratio, -e), ldexpf(1.0f, e)};
 }
 
-// c is 1 exactly, and x its own result, for all norms up to max_norm; a NaN
-// norm makes c, and so every gradient, NaN.  in may be out.  Everything passes
+// c is 1 exactly, and x its own result, where norm + eps <= max_norm (and where
+// the ratio rounds to 1: 2^-25 below it); a NaN norm makes c, and so every
+// gradient, NaN.  in may be out.  Everything passes
 // here once: past the caches (2.1 GB of norm, read and write 516 us, 564 through
 // them; 134 MB of gradients 64 and 66; what then reads the gradients loses 1% at
 // most).  The norm's pass keeps its loads in them for this one: nontemporal there

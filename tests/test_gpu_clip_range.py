@@ -54,3 +54,25 @@ def test_factors_below_the_normal_range(gpu_lib, scale, max_norm):
     out = [torch.full_like(t, 9.0) for t in many]
     gpu_lib.clip_grads(many, max_norm, out=out)
     _check(many, out, want)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_norms_next_to_max_norm(gpu_lib, dtype):
+    """The factor is max_norm / (norm + eps): below 1 for a norm of max_norm itself, 1 without eps, and 1 for norms
+    that are eps or more below; in place and with outputs of their own."""
+    t0 = [torch.full((16,), v, dtype=dtype, device="cuda") for v in (0.5, -0.75, 1.5)]   # norm^2 = 49
+    eps = 2.0 ** -10
+    for max_norm, e, factor in ((7.0, eps, 7.0 / (7.0 + eps)), (7.0, 0.0, 1.0), (7.0 + eps, eps, 1.0),
+                                (7.0 + 2 * eps, eps, 1.0), (6.5, 0.0, 6.5 / 7.0), (7.0, 1e-9, 1.0)):
+        want = [(t.double() * factor) for t in t0]
+        ts, out = [t.clone() for t in t0], [torch.full_like(t, 9.0) for t in t0]
+        n = gpu_lib.clip_grads(ts, max_norm, e, out=out)
+        assert float(n) == 7.0 and all(torch.equal(a, b) for a, b in zip(ts, t0))
+        if factor == 1.0:
+            assert all(torch.equal(a, b) for a, b in zip(out, t0))
+        else:
+            _check(ts, out, [_np(w) for w in want])
+            if dtype is torch.float32:
+                assert not any((a == b).any() for a, b in zip(out, t0))
+        gpu_lib.clip_grads(ts, max_norm, e)
+        assert all(torch.equal(a, b) for a, b in zip(ts, out))
