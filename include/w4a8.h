@@ -568,7 +568,9 @@ int w4a8_swiglu_backward(const uint8_t* ckpt_fp8_dev, const float* ckpt_scales_d
  *   per (row, 128 columns): s = amax|y| / 448 (1 where amax < 2^-100), code =
  *   E4M3FN round-to-nearest-even of y * (1/s): the input of w4a8_grouped_gemm.
  * The norm is of h as it is stored, so that the next layer and the backward
- * pass see the values it was taken of.
+ * pass see the values it was taken of.  y is within 2^-21 of the formula's, so a
+ * quotient that lies on the border of two codes (exact halves are common: bf16 h
+ * and weights) may get either.
  *
  * x_bf16_dev         bf16 [T][K].
  * residual_bf16_dev  bf16 [T][K] or NULL.
@@ -606,7 +608,8 @@ int w4a8_rms_norm(const uint16_t* x_bf16_dev, const uint16_t* residual_bf16_dev,
  * dweight_dev    out fp32 [K], or NULL.
  * workspace_dev  w4a8_rms_norm_backward_bytes(T, K) bytes, 4-byte aligned, not
  *                shared by calls that may run at a time.
- * Every run gives the same bits.  Limits and alignment as w4a8_rms_norm.
+ * Every run gives the same bits.  The products dy * weight are in fp32: past its
+ * range their row is infinite or NaN.  Limits and alignment as w4a8_rms_norm.
  * T == 0 writes zeros to dweight.
  */
 int w4a8_rms_norm_backward(const uint16_t* h_bf16_dev, const void* weight_dev, int weight_type,

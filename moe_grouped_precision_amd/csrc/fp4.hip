@@ -12,9 +12,9 @@
 //
 // Streams: a thread holds 16 columns, i.e. an NVFP4 group, two threads an MX
 // group.  Bound by HBM, 264 M weights: the experts' amax 91 us (5.8 TB/s), NVFP4
-// from it 120 (5.6), back 112 (6.0).  Tried: the weights read the second time past
-// the caches, 4% slower from 16 experts of 4096 x 4096 on; from the end, where the
-// amax pass left off, 3%.
+// from it 120 (5.6), back 112 (6.0); MXFP4 111 (6.0), back 127 (5.3).  Tried: NVFP4's
+// weights read the second time past the caches, 4% slower from 16 experts of 4096 x
+// 4096 on; from the end, where the amax pass left off, 3%.
 #include "swiglu.h"
 #include "w4a8_launch.h"
 

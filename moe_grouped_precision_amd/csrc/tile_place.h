@@ -14,7 +14,9 @@
 namespace w4a8 {
 
 // Tiles (steps) of `size` that n rows (z) take; n >= 0.
-W4A8_HD constexpr int pieces_of(int n, int size) { return (int)(((uint32_t)n + (uint32_t)(size - 1)) / (uint32_t)size); }
+W4A8_HD constexpr int pieces_of(int n, int size) {
+  return (int)(((uint32_t)n + (uint32_t)(size - 1)) / (uint32_t)size);
+}
 
 // Rows of each tile where `rows` go to `tiles` tiles evenly, in whole blocks of
 // 16; with tiles = pieces_of(rows, T) and T a multiple of 16, at most T, and the
